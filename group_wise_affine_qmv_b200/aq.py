@@ -51,7 +51,8 @@ class AqPlan(ctypes.Structure):
 
 
 EXPORTED = ("aq_quantize", "aq_dequantize", "aq_dequantize_rows", "aq_qmv", "aq_qmm_t", "aq_qmm_t_grouped", "aq_qmv_gathered", "aq_qmm_t_multi",
-            "aq_qmm_t_swiglu", "aq_qmm_t_residual", "aq_plan_linear", "aq_status_string", "aq_last_error_message",
+            "aq_qmm_t_swiglu", "aq_qmm_t_residual", "aq_kv_append", "aq_kv_attention", "aq_kv_attention_workspace",
+            "aq_plan_linear", "aq_status_string", "aq_last_error_message",
             "aq_device_error", "aq_check_bounded_wait", "aq_version")
 
 _lib = None
@@ -90,6 +91,13 @@ def load_library(path: str = LIB_PATH):
         lib.aq_qmm_t_swiglu.restype = ci
         lib.aq_qmm_t_residual.argtypes = [V, V, V, V, ci, ci, V, V, vp]
         lib.aq_qmm_t_residual.restype = ci
+        lib.aq_kv_append.argtypes = [V, V, vp, ci, ci] + [V] * 8 + [vp]
+        lib.aq_kv_append.restype = ci
+        lib.aq_kv_attention_workspace.argtypes = [V, V, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.aq_kv_attention_workspace.restype = ci
+        lib.aq_kv_attention.argtypes = [V] * 7 + [ci, ci, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, ci, V, vp,
+                                                  ctypes.c_size_t, vp]
+        lib.aq_kv_attention.restype = ci
         lib.aq_plan_linear.argtypes = [V, V, V, V, ci, ci, V, ci, ctypes.POINTER(AqPlan)]
         lib.aq_plan_linear.restype = ci
         lib.aq_status_string.argtypes = [ci]
@@ -277,6 +285,56 @@ def aq_qmv_gathered(x, x_ids, w_ids, wq_bank, s_bank, b_bank, group: int, bits: 
         _check(lib, lib.aq_qmv_gathered(view(x), ctypes.c_void_p(x_ids.data_ptr()), ctypes.c_void_p(w_ids.data_ptr()),
                                         R, view(wq_bank), view(s_bank), view(b_bank), group, bits, view(out),
                                         _stream(x)))
+    return out
+
+
+def _ids(t: torch.Tensor, name: str, dim: int, device):
+    if t.dtype != torch.int64 or t.device != device or t.dim() != dim:
+        raise TypeError(f"{name} must be a {dim}D int64 tensor on {device}")
+    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise TypeError(f"{name} must be contiguous")
+    return t
+
+
+def aq_kv_append(k, v, slots, k_cache, v_cache, group: int, bits: int, k_out=None, v_out=None):
+    """New keys and values [T, H, D] into a paged cache: token t goes to slot slots[t] = page * S + offset
+    (negative: not stored).  k_cache, v_cache = (wq [P, H, S, D*bits/32], scales, biases [P, H, S, D/group]),
+    written in place.  k_out, v_out [T, H, D]: the values that the cache then stands for."""
+    lib = load_library()
+    _ids(slots, "slots", 1, k.device)
+    if slots.numel() != k.shape[0]:
+        raise ValueError("one slot per token")
+    with torch.cuda.device(k.device):
+        _check(lib, lib.aq_kv_append(view(k), view(v), ctypes.c_void_p(slots.data_ptr()), group, bits,
+                                     *[view(t) for t in (*k_cache, *v_cache)],
+                                     None if k_out is None else view(k_out), None if v_out is None else view(v_out),
+                                     _stream(k)))
+
+
+def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, scale: float | None = None,
+                    window: int = 0, out=None):
+    """Attention of q [B, Tq, Hq, D] over a paged cache (as aq_kv_append fills it): sequence b holds lengths[b]
+    tokens, the Tq of q the last ones, in pages pages[b, :] [B, max_pages]; query i sees the tokens up to its own
+    (window > 0: the last `window` of them).  scale: 1 / sqrt(D) if not given."""
+    lib = load_library()
+    _ids(pages, "pages", 2, q.device)
+    _ids(lengths, "lengths", 1, q.device)
+    if pages.shape[0] != q.shape[0] or lengths.shape[0] != q.shape[0]:
+        raise ValueError("pages and lengths need one entry per sequence")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    vq, vk = view(q), view(k_cache[0])
+    need = ctypes.c_size_t()
+    with torch.cuda.device(q.device):
+        stream = _stream(q)
+        _check(lib, lib.aq_kv_attention_workspace(vq, vk, pages.shape[1], ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        _check(lib, lib.aq_kv_attention(vq, vk, *[view(t) for t in (*k_cache[1:], *v_cache)], group, bits,
+                                        ctypes.c_void_p(pages.data_ptr()), pages.stride(0), pages.shape[1],
+                                        ctypes.c_void_p(lengths.data_ptr()), float(scale), int(window), view(out),
+                                        ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream))
     return out
 
 

@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "aq_internal.h"
+#include "kv_cache.h"
 
 #define AQ_API extern "C" __attribute__((visibility("default")))
 
@@ -456,6 +457,103 @@ aq_status check_quant_views(const aq_view* w, int group, int bits, const aq_view
             return fail(AQ_ERR_OVERLAP, "quantize outputs overlap each other or the input");
     }
     return AQ_OK;
+}
+
+// ---------------------------------------------------------------------------
+// the 4-bit key/value cache
+// ---------------------------------------------------------------------------
+
+// Whether two views of the same shape and strides interleave without meeting (the key and value
+// halves of one buffer): together they are one more dimension of extent 2, whose stride is their
+// distance.
+bool interleave(const aq_view* a, const aq_view* b) {
+    if (a->rank != b->rank || a->dtype != b->dtype) return false;
+    int64_t st[5], n[5];
+    int k = 0;
+    for (int i = 0; i < a->rank; ++i) {
+        if (a->shape[i] != b->shape[i]) return false;
+        if (a->shape[i] <= 1) continue;
+        if (a->stride[i] != b->stride[i]) return false;
+        st[k] = a->stride[i];
+        n[k++] = a->shape[i];
+    }
+    const uintptr_t pa = (uintptr_t)a->data, pb = (uintptr_t)b->data;
+    const uintptr_t dist = pa < pb ? pb - pa : pa - pb;
+    if (dist % elem_size(a->dtype) != 0) return false;
+    st[k] = (int64_t)(dist / elem_size(a->dtype));
+    n[k++] = 2;
+    for (int i = 1; i < k; ++i)
+        for (int j = i; j > 0 && st[j] < st[j - 1]; --j) {
+            std::swap(st[j], st[j - 1]);
+            std::swap(n[j], n[j - 1]);
+        }
+    int64_t reach = 0;
+    for (int i = 0; i < k; ++i) {
+        if (st[i] <= reach) return false;
+        reach += (n[i] - 1) * st[i];
+    }
+    return true;
+}
+
+// One side of a cache: [P, H, S, D/8] words with scales and biases [P, H, S, D/G] of dtype dt.
+aq_status check_cache_side(const aq_view* wq, const aq_view* sc, const aq_view* bi, const char* name, int dt, int64_t D,
+                           int group, aq::kv::Side* out) {
+    aq_status st;
+    if ((st = check_view(wq, name, 4, 4)) != AQ_OK) return st;
+    if ((st = check_view(sc, name, 4, 4)) != AQ_OK) return st;
+    if ((st = check_view(bi, name, 4, 4)) != AQ_OK) return st;
+    if (wq->dtype != AQ_U32) return fail(AQ_ERR_DTYPE, "%s: codes must be u32", name);
+    if (sc->dtype != dt || bi->dtype != dt) return fail(AQ_ERR_DTYPE, "%s: scales/biases must have the activations' dtype", name);
+    if (wq->shape[3] != D / 8) return fail(AQ_ERR_SHAPE, "%s: codes must be [pages, heads, slots, D/8 = %lld]", name, (long long)(D / 8));
+    for (int i = 0; i < 3; ++i)
+        if (sc->shape[i] != wq->shape[i] || bi->shape[i] != wq->shape[i])
+            return fail(AQ_ERR_SHAPE, "%s: scales/biases leading dims must equal the codes'", name);
+    if (sc->shape[3] != D / group || bi->shape[3] != D / group)
+        return fail(AQ_ERR_SHAPE, "%s: scales/biases last dim must be D/group = %lld", name, (long long)(D / group));
+    if (numel(wq) > 0) {
+        if (!aligned16(wq->data)) return fail(AQ_ERR_ALIGN, "%s: codes must be 16-byte aligned", name);
+        for (int i = 0; i < 3; ++i)
+            if (wq->shape[i] > 1 && wq->stride[i] % 4 != 0)
+                return fail(AQ_ERR_ALIGN, "%s: strides of the codes must keep rows 16-byte aligned", name);
+    }
+    auto stride = [](const aq_view* v, int i) { return v->shape[i] > 1 ? v->stride[i] : 0; };
+    out->wq = (uint32_t*)wq->data;
+    out->scales = (uint16_t*)sc->data;
+    out->biases = (uint16_t*)bi->data;
+    out->w_page = stride(wq, 0); out->w_head = stride(wq, 1); out->w_slot = stride(wq, 2);
+    out->s_page = stride(sc, 0); out->s_head = stride(sc, 1); out->s_slot = stride(sc, 2);
+    out->b_page = stride(bi, 0); out->b_head = stride(bi, 1); out->b_slot = stride(bi, 2);
+    return AQ_OK;
+}
+
+aq_status check_cache_bits(int bits, int group) {
+    aq_status st = check_bits_group(bits, group);
+    if (st != AQ_OK) return st;
+    if (bits != 4) return fail(AQ_ERR_UNSUPPORTED, "key/value caches hold 4-bit codes (bits=%d)", bits);
+    return AQ_OK;
+}
+
+// what the attention call and its workspace query share: shapes of q and the cache
+aq_status check_attention_q(const aq_view* q, const aq_view* k_wq, int64_t max_pages) {
+    aq_status st;
+    if ((st = check_view(q, "q", 4, 4)) != AQ_OK) return st;
+    if ((st = check_view(k_wq, "k cache", 4, 4)) != AQ_OK) return st;
+    if (!is_half(q->dtype)) return fail(AQ_ERR_DTYPE, "q must be bf16 or f16");
+    const int64_t B = q->shape[0], Tq = q->shape[1], Hq = q->shape[2], D = q->shape[3];
+    const int64_t H = k_wq->shape[1], S = k_wq->shape[2];
+    if (D != 64 && D != 128 && D != 256) return fail(AQ_ERR_UNSUPPORTED, "head size %lld (64, 128 and 256 are supported)", (long long)D);
+    if (H < 1 || Hq % H != 0) return fail(AQ_ERR_SHAPE, "%lld query heads are not a multiple of %lld key/value heads", (long long)Hq, (long long)H);
+    if (max_pages < 0) return fail(AQ_ERR_SHAPE, "max_pages < 0");
+    if (max_pages > 0x7fffffff || S > 0x7fffffff || max_pages * S > 0x7fffffff)
+        return fail(AQ_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens per sequence");
+    if (B > 65535 || H > 65535 || Hq / H > (1 << 20) || Tq > (1 << 20) || Hq / H * Tq > (1 << 20))
+        return fail(AQ_ERR_UNSUPPORTED, "more than 65535 sequences or heads, or 2^20 query rows per key/value head");
+    return AQ_OK;
+}
+
+aq::kv::AttnShape attention_shape(const aq_view* q, const aq_view* k_wq, int64_t max_pages) {
+    const int64_t H = k_wq->shape[1];
+    return aq::kv::attn_shape(q->shape[0], q->shape[2] / H * q->shape[1], H, (int)q->shape[3], max_pages * k_wq->shape[2]);
 }
 
 }  // namespace
@@ -918,5 +1016,170 @@ AQ_API aq_status aq_check_bounded_wait(uint64_t budget_ns, void* stream) {
     if (st != AQ_OK) return st;
     cudaError_t e = aq::launch_bounded_wait_check(budget_ns, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "bounded-wait check launch");
+    return AQ_OK;
+}
+
+AQ_API aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots, int group, int bits,
+                              const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases, const aq_view* v_wq,
+                              const aq_view* v_scales, const aq_view* v_biases, const aq_view* k_out, const aq_view* v_out,
+                              void* stream) {
+    g_msg[0] = 0;
+    aq_status st;
+    if ((st = check_view(k, "k", 3, 3)) != AQ_OK) return st;
+    if ((st = check_view(v, "v", 3, 3)) != AQ_OK) return st;
+    if ((st = check_cache_bits(bits, group)) != AQ_OK) return st;
+    if (!is_half(k->dtype) || v->dtype != k->dtype) return fail(AQ_ERR_DTYPE, "k and v must be bf16 or f16 (same dtype)");
+    const int64_t T = k->shape[0], H = k->shape[1], D = k->shape[2];
+    if (v->shape[0] != T || v->shape[1] != H || v->shape[2] != D) return fail(AQ_ERR_SHAPE, "v must have k's shape");
+    if (D % group != 0) return fail(AQ_ERR_GROUP, "head size %lld not a multiple of group=%d", (long long)D, group);
+    aq::kv::AppendArgs a;
+    memset(&a, 0, sizeof a);
+    if ((st = check_cache_side(k_wq, k_scales, k_biases, "k cache", k->dtype, D, group, &a.side[0])) != AQ_OK) return st;
+    if ((st = check_cache_side(v_wq, v_scales, v_biases, "v cache", k->dtype, D, group, &a.side[1])) != AQ_OK) return st;
+    if (k_wq->shape[1] != H) return fail(AQ_ERR_SHAPE, "the cache must have k's %lld heads", (long long)H);
+    for (int i = 0; i < 3; ++i)
+        if (v_wq->shape[i] != k_wq->shape[i]) return fail(AQ_ERR_SHAPE, "the v cache must have the k cache's shape");
+    const aq_view* outs[8] = {k_wq, k_scales, k_biases, v_wq, v_scales, v_biases, k_out, v_out};
+    const aq_view* ins[2] = {k, v};
+    for (int j = 0; j < 2; ++j) {
+        const aq_view* o = outs[6 + j];
+        if (!o) continue;
+        if ((st = check_view(o, j ? "v_out" : "k_out", 3, 3)) != AQ_OK) return st;
+        if (o->dtype != k->dtype) return fail(AQ_ERR_DTYPE, "k_out/v_out must have k's dtype");
+        if (o->shape[0] != T || o->shape[1] != H || o->shape[2] != D) return fail(AQ_ERR_SHAPE, "k_out/v_out must have k's shape");
+    }
+    for (int i = 0; i < 8; ++i) {
+        if (!outs[i]) continue;
+        if ((st = check_output(outs[i], i < 6 ? "cache" : "k_out/v_out")) != AQ_OK) return st;
+        for (int j = 0; j < 2; ++j)
+            if (overlaps(outs[i], ins[j])) return fail(AQ_ERR_OVERLAP, "an output overlaps k or v");
+        for (int j = 0; j < i; ++j)
+            if (outs[j] && overlaps(outs[i], outs[j]) && !interleave(outs[i], outs[j]))
+                return fail(AQ_ERR_OVERLAP, "outputs overlap each other");
+    }
+    if (T == 0 || H == 0 || D == 0) return AQ_OK;
+    if (!slots) return fail(AQ_ERR_NULL, "slots is NULL");
+    if (H * (D / 8) > (1 << 24) || k_wq->shape[2] > 0x7fffffff) return fail(AQ_ERR_UNSUPPORTED, "rows too large");
+    if ((st = check_device()) != AQ_OK) return st;
+    for (int j = 0; j < 2; ++j) {
+        const aq_view *x = ins[j], *o = outs[6 + j];
+        auto vec = [&](const aq_view* t) {
+            return aligned16(t->data) && (T <= 1 || t->stride[0] % 8 == 0) && (H <= 1 || t->stride[1] % 8 == 0);
+        };
+        a.x[j] = (const uint16_t*)x->data;
+        a.x_tok[j] = x->stride[0];
+        a.x_head[j] = x->stride[1];
+        a.xvec[j] = vec(x) ? 1 : 0;
+        if (o) {
+            a.out[j] = (uint16_t*)o->data;
+            a.o_tok[j] = o->stride[0];
+            a.o_head[j] = o->stride[1];
+            a.ovec[j] = vec(o) ? 1 : 0;
+        }
+    }
+    a.slots = slots;
+    a.T = T;
+    a.H = (int)H;
+    a.D = (int)D;
+    a.S = (int)k_wq->shape[2];
+    a.nslots = k_wq->shape[0] * k_wq->shape[2];
+    a.log2g = log2i(group);
+    cudaError_t e = aq::device_error_ptr(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = aq::kv::launch_append(a, k->dtype == AQ_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+    return AQ_OK;
+}
+
+AQ_API aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64_t max_pages, size_t* bytes) {
+    g_msg[0] = 0;
+    if (!bytes) return fail(AQ_ERR_NULL, "bytes is NULL");
+    aq_status st = check_attention_q(q, k_wq, max_pages);
+    if (st != AQ_OK) return st;
+    const aq::kv::AttnShape s = attention_shape(q, k_wq, max_pages);
+    *bytes = numel(q) > 0 && s.split ? (s.o_floats + s.ml_floats) * sizeof(float) : 0;
+    return AQ_OK;
+}
+
+AQ_API aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases,
+                                 const aq_view* v_wq, const aq_view* v_scales, const aq_view* v_biases, int group, int bits,
+                                 const int64_t* pages, int64_t pages_row, int64_t max_pages, const int64_t* lengths,
+                                 float scale, int window, const aq_view* out, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    g_msg[0] = 0;
+    aq_status st;
+    if ((st = check_attention_q(q, k_wq, max_pages)) != AQ_OK) return st;
+    if ((st = check_cache_bits(bits, group)) != AQ_OK) return st;
+    const int64_t B = q->shape[0], Tq = q->shape[1], Hq = q->shape[2], D = q->shape[3], H = k_wq->shape[1];
+    if (D % group != 0) return fail(AQ_ERR_GROUP, "head size %lld not a multiple of group=%d", (long long)D, group);
+    aq::kv::AttnArgs a;
+    memset(&a, 0, sizeof a);
+    if ((st = check_cache_side(k_wq, k_scales, k_biases, "k cache", q->dtype, D, group, &a.k)) != AQ_OK) return st;
+    if ((st = check_cache_side(v_wq, v_scales, v_biases, "v cache", q->dtype, D, group, &a.v)) != AQ_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if (v_wq->shape[i] != k_wq->shape[i]) return fail(AQ_ERR_SHAPE, "the v cache must have the k cache's shape");
+    if ((st = check_view(out, "out", 4, 4)) != AQ_OK) return st;
+    if (out->dtype != q->dtype) return fail(AQ_ERR_DTYPE, "out must have q's dtype");
+    for (int i = 0; i < 4; ++i)
+        if (out->shape[i] != q->shape[i]) return fail(AQ_ERR_SHAPE, "out must have q's shape");
+    if ((st = check_output(out, "out")) != AQ_OK) return st;
+    if (window < 0) return fail(AQ_ERR_SHAPE, "window < 0");
+    if (!(scale - scale == 0.0f)) return fail(AQ_ERR_SHAPE, "scale must be finite");
+    const aq::kv::AttnShape s = attention_shape(q, k_wq, max_pages);
+    const size_t need = numel(q) > 0 && s.split ? (s.o_floats + s.ml_floats) * sizeof(float) : 0;
+    aq_view ws;
+    memset(&ws, 0, sizeof ws);
+    ws.data = workspace;
+    ws.dtype = AQ_F32;
+    ws.rank = 1;
+    ws.shape[0] = (int64_t)(need / 4);
+    ws.stride[0] = 1;
+    const aq_view* ins[7] = {q, k_wq, k_scales, k_biases, v_wq, v_scales, v_biases};
+    for (const aq_view* v : ins) {
+        if (overlaps(out, v)) return fail(AQ_ERR_OVERLAP, "out overlaps an input");
+        if (need && overlaps(&ws, v)) return fail(AQ_ERR_OVERLAP, "the workspace overlaps an input");
+    }
+    if (need && overlaps(&ws, out)) return fail(AQ_ERR_OVERLAP, "the workspace overlaps out");
+    if (numel(q) == 0) return AQ_OK;
+    if (need) {
+        if (!workspace) return fail(AQ_ERR_NULL, "workspace is NULL");
+        if (workspace_bytes < need)
+            return fail(AQ_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(AQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+    }
+    if (!lengths || (!pages && max_pages > 0)) return fail(AQ_ERR_NULL, "pages / lengths is NULL");
+    if (pages_row < 0) return fail(AQ_ERR_STRIDE, "pages_row < 0");
+    if ((st = check_device()) != AQ_OK) return st;
+    const int64_t S = k_wq->shape[2], kg = D / group;
+    a.q = (const uint16_t*)q->data;
+    a.q_b = q->stride[0]; a.q_t = q->stride[1]; a.q_h = q->stride[2];
+    a.out = (uint16_t*)out->data;
+    a.o_b = out->stride[0]; a.o_t = out->stride[1]; a.o_h = out->stride[2];
+    a.ovec = ((uintptr_t)out->data & 7) == 0 && (B <= 1 || a.o_b % 4 == 0) && (Tq <= 1 || a.o_t % 4 == 0) &&
+             (Hq <= 1 || a.o_h % 4 == 0);
+    a.pages = pages;
+    a.pages_row = pages_row;
+    a.max_pages = max_pages;
+    a.P = k_wq->shape[0];
+    a.lengths = lengths;
+    a.B = (int)B; a.Tq = (int)Tq; a.Hq = (int)Hq; a.Hkv = (int)H; a.S = (int)S;
+    a.rep = (int)(Hq / H);
+    a.rows = (int)(Hq / H * Tq);
+    a.rtiles = s.rtiles;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    // tiles of 16 tokens copy as whole pieces: pages of whole tiles, scales and biases dense per head and page
+    bool fast = S > 0 && S % 16 == 0;
+    for (const aq::kv::Side* d : {&a.k, &a.v})
+        fast = fast && d->s_slot == kg && d->b_slot == kg && aligned16(d->scales) && aligned16(d->biases) &&
+               d->s_page % 8 == 0 && d->s_head % 8 == 0 && d->b_page % 8 == 0 && d->b_head % 8 == 0;
+    a.fast = fast ? 1 : 0;
+    a.split = s.split;
+    a.part_o = (float*)workspace;
+    a.part_ml = (float*)workspace + s.o_floats;
+    cudaError_t e = aq::device_error_ptr(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = aq::kv::launch_attention(a, s, (int)D, group, q->dtype == AQ_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
     return AQ_OK;
 }

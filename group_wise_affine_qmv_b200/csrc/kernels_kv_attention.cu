@@ -1,0 +1,48 @@
+// kernels_kv_attention.cu -- launch shape of the attention over a 4-bit cache, and the choice of its
+// instantiation.
+#include "kv_cache.h"
+
+namespace aq {
+namespace kv {
+
+template <int D, bool BF>
+cudaError_t launch_d(const AttnArgs& a, const AttnShape& s, int group, cudaStream_t st);
+extern template cudaError_t launch_d<64, true>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+extern template cudaError_t launch_d<64, false>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+extern template cudaError_t launch_d<128, true>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+extern template cudaError_t launch_d<128, false>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+extern template cudaError_t launch_d<256, true>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+extern template cudaError_t launch_d<256, false>(const AttnArgs&, const AttnShape&, int, cudaStream_t);
+
+namespace {
+constexpr int SMS = 148;
+constexpr int UNIT_TOKENS = 64;   // tokens per unit (kv_attention_kernel.cuh)
+}  // namespace
+
+AttnShape attn_shape(int64_t B, int64_t rows, int64_t Hkv, int D, int64_t max_tokens) {
+    AttnShape s;
+    s.nt = rows <= 8 ? 1 : (rows <= 16 || D == 256) ? 2 : 4;
+    s.rtiles = (int)((rows + 8 * s.nt - 1) / (8 * s.nt));
+    const int64_t items = B * Hkv * s.rtiles;
+    // CTAs that fit the device at once (the kernel's launch bounds)
+    const int per_sm = (D == 256 || s.nt == 4) ? 2 : s.nt == 2 ? 3 : 4;
+    const int64_t all = (int64_t)SMS * per_sm;
+    const int64_t most = items * ((max_tokens + UNIT_TOKENS - 1) / UNIT_TOKENS);
+    s.split = 1;
+    s.grid = (int)(most < all ? (most < 1 ? 1 : most) : all);
+    s.o_floats = (size_t)2 * s.grid * 8 * s.nt * D;
+    s.ml_floats = (size_t)2 * s.grid * 8 * s.nt * 2;
+    return s;
+}
+
+cudaError_t launch_attention(const AttnArgs& a, const AttnShape& s, int D, int group, bool bf16, cudaStream_t st) {
+    switch (D) {
+        case 64: return bf16 ? launch_d<64, true>(a, s, group, st) : launch_d<64, false>(a, s, group, st);
+        case 128: return bf16 ? launch_d<128, true>(a, s, group, st) : launch_d<128, false>(a, s, group, st);
+        case 256: return bf16 ? launch_d<256, true>(a, s, group, st) : launch_d<256, false>(a, s, group, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace kv
+}  // namespace aq

@@ -50,6 +50,7 @@
 #ifndef AQ_H
 #define AQ_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -283,6 +284,70 @@ aq_status aq_qmm_t_swiglu(const aq_view* x, const aq_view* wq_gate, const aq_vie
 aq_status aq_qmm_t_residual(const aq_view* x, const aq_view* wq, const aq_view* scales,
                             const aq_view* biases, int group, int bits, const aq_view* r,
                             const aq_view* y, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Attention between the projections: a paged key/value cache of 4-bit     */
+/* codes.                                                                  */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * A cache holds keys (and, in tensors of its own, values) in the library's format, groups along
+ * the head size D: codes [P, H, S, D/8] AQ_U32, scales and biases [P, H, S, D/group] in the
+ * activations' dtype; P pages of S slots, H key/value heads.  Pages, heads and slots may have any
+ * strides that keep the rows of codes 16-byte aligned (so [P, S, H, ..] storage works as a
+ * transposed view); dense scales and biases per page and head, and S a multiple of 16, are the
+ * fast layout.  Slot s of page p has the flat index p * S + s.
+ * bits must be 4 (AQ_ERR_UNSUPPORTED otherwise).
+ */
+
+/*
+ * aq_kv_append -- quantize the keys and values of T new tokens into their slots, exactly as
+ *   aq_quantize does (scale = (max - min) / 15, bias = min, ties to even, in fp32; scale and bias
+ *   then rounded), both in one launch.
+ * k, v: [T, H, D] AQ_BF16 or AQ_F16, any strides of tokens and heads (slices of one projection's
+ *   output); D a multiple of group.  Finite values, as for aq_quantize.
+ * slots: DEVICE pointer to T int64 flat slots.  A negative slot is not stored (padding).  A slot
+ *   of P * S or more is not stored either and sets the device error AQ_ERR_INDEX.  No slot may
+ *   appear twice in one call (it would hold parts of both tokens).
+ * k_out, v_out: optional (NULL) [T, H, D] in k's dtype: scale * q + bias of the stored scale and
+ *   bias, evaluated in fp32 and rounded once, for every token (stored or not) -- what the cache
+ *   now stands for, so that a prompt's own attention can use what later steps will read.
+ * Slots that no token names are left as they are.  The outputs must not overlap k, v or each
+ * other (key and value halves of one buffer may interleave).
+ */
+aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots, int group, int bits,
+                       const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases,
+                       const aq_view* v_wq, const aq_view* v_scales, const aq_view* v_biases,
+                       const aq_view* k_out, const aq_view* v_out, void* stream);
+
+/*
+ * aq_kv_attention -- attention of a few new tokens per sequence over the cache:
+ *     out[b, i, h] = sum_j softmax_j(scale * q[b, i, h] . k_j) v_j
+ *   over the cached tokens j of sequence b that query i sees: it sits at position
+ *   n = lengths[b] - Tq + i and sees j <= n, with window > 0 only n - window < j.  Query head h
+ *   reads key/value head h / (Hq / H).
+ * q, out: [B, Tq, Hq, D] AQ_BF16 or AQ_F16 (any strides of the first three dims), D 64, 128 or
+ *   256, Hq a multiple of H, scales and biases in q's dtype.
+ * lengths: DEVICE pointer to B int64, tokens per sequence with the Tq new ones (append them
+ *   first).  A sequence shorter than Tq leaves its first Tq - lengths[b] queries without a token
+ *   to see; a query that sees nothing gives zeros.
+ * pages: DEVICE pointer to int64 page ids, row b (at pages + b * pages_row) the pages of sequence
+ *   b in order, max_pages of them; entries past a sequence's last page are not read.  A length
+ *   outside [0, max_pages * S] is clamped, a page id outside [0, P) drops the tokens around it;
+ *   both set the device error AQ_ERR_INDEX, and neither reads outside the cache.  Slots past a
+ *   sequence's end may hold anything, NaN scales included.
+ * workspace: DEVICE memory of at least the bytes aq_kv_attention_workspace gives for the same q,
+ *   k_wq and max_pages, 16-byte aligned, used by this call only while it runs on its stream.
+ * Scores, softmax statistics and sums are fp32; the query is exact, the product of a
+ * probability and a value's scale is rounded to 11 bits.  Meant for decode and short runs of new
+ * tokens: the cache is read once per 32 query rows (D 256: 16) of a key/value head.
+ */
+aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases,
+                          const aq_view* v_wq, const aq_view* v_scales, const aq_view* v_biases, int group,
+                          int bits, const int64_t* pages, int64_t pages_row, int64_t max_pages,
+                          const int64_t* lengths, float scale, int window, const aq_view* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64_t max_pages, size_t* bytes);
 
 /* ---------------------------------------------------------------------- */
 /* Introspection (host only, no GPU work).                                 */

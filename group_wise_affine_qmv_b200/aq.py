@@ -52,7 +52,7 @@ class AqPlan(ctypes.Structure):
 
 EXPORTED = ("aq_quantize", "aq_dequantize", "aq_dequantize_rows", "aq_qmv", "aq_qmm_t", "aq_qmm_t_grouped", "aq_qmv_gathered", "aq_qmm_t_multi",
             "aq_qmm_t_swiglu", "aq_qmm_t_residual", "aq_kv_append", "aq_kv_attention", "aq_kv_attention_workspace",
-            "aq_plan_linear", "aq_status_string", "aq_last_error_message",
+            "aq_moe_swiglu", "aq_moe_swiglu_workspace", "aq_plan_linear", "aq_status_string", "aq_last_error_message",
             "aq_device_error", "aq_check_bounded_wait", "aq_version")
 
 _lib = None
@@ -98,6 +98,10 @@ def load_library(path: str = LIB_PATH):
         lib.aq_kv_attention.argtypes = [V] * 7 + [ci, ci, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, ci, V, vp,
                                                   ctypes.c_size_t, vp]
         lib.aq_kv_attention.restype = ci
+        lib.aq_moe_swiglu_workspace.argtypes = [ctypes.c_int64, ci, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.aq_moe_swiglu_workspace.restype = ci
+        lib.aq_moe_swiglu.argtypes = [V, V, ci, ci] + [V] * 9 + [ci, ci, ctypes.c_float, V, V, vp, ctypes.c_size_t, vp]
+        lib.aq_moe_swiglu.restype = ci
         lib.aq_plan_linear.argtypes = [V, V, V, V, ci, ci, V, ci, ctypes.POINTER(AqPlan)]
         lib.aq_plan_linear.restype = ci
         lib.aq_status_string.argtypes = [ci]
@@ -335,6 +339,26 @@ def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, 
                                         ctypes.c_void_p(pages.data_ptr()), pages.stride(0), pages.shape[1],
                                         ctypes.c_void_p(lengths.data_ptr()), float(scale), int(window), view(out),
                                         ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream))
+    return out
+
+
+def aq_moe_swiglu(x, logits, top_k: int, gate, up, down, group: int, bits: int, norm_topk: bool = True,
+                  rms_eps: float = 0.0, residual=None, out=None, out_dtype=None):
+    """A whole mixture-of-experts layer for up to 64 tokens: top_k experts of logits [T, E] per token, their gated
+    MLPs (gate, up [E, N, K], down [E, K, N] as (wq, scales, biases)) weighted and added, plus the residual.
+    rms_eps > 0: x RMS-normalised per token first.  out may be residual or x itself."""
+    lib = load_library()
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    need = ctypes.c_size_t()
+    with torch.cuda.device(x.device):
+        stream = _stream(x)
+        _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, gate[0].shape[-2], ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        _check(lib, lib.aq_moe_swiglu(view(x), view(logits), top_k, 1 if norm_topk else 0,
+                                      *[view(t) for t in (*gate, *up, *down)], group, bits, float(rms_eps),
+                                      None if residual is None else view(residual), view(out),
+                                      ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream))
     return out
 
 

@@ -18,6 +18,7 @@
 
 #include "aq_internal.h"
 #include "kv_cache.h"
+#include "moe.h"
 
 #define AQ_API extern "C" __attribute__((visibility("default")))
 
@@ -554,6 +555,58 @@ aq_status check_attention_q(const aq_view* q, const aq_view* k_wq, int64_t max_p
 aq::kv::AttnShape attention_shape(const aq_view* q, const aq_view* k_wq, int64_t max_pages) {
     const int64_t H = k_wq->shape[1];
     return aq::kv::attn_shape(q->shape[0], q->shape[2] / H * q->shape[1], H, (int)q->shape[3], max_pages * k_wq->shape[2]);
+}
+
+// ---------------------------------------------------------------------------
+// the mixture-of-experts layer
+// ---------------------------------------------------------------------------
+
+bool same_view(const aq_view* a, const aq_view* b) {
+    return a->data == b->data && a->dtype == b->dtype && a->rank == b->rank &&
+           memcmp(a->shape, b->shape, sizeof(int64_t) * a->rank) == 0 &&
+           memcmp(a->stride, b->stride, sizeof(int64_t) * a->rank) == 0;
+}
+
+// One expert bank: [E, rows, K*bits/32] words with dense scale/bias rows [E, rows, K/group] of dtype dt.
+aq_status check_bank(const aq_view* wq, const aq_view* sc, const aq_view* bi, const char* name, int dt, int64_t E, int64_t rows,
+                     int64_t K, int group, int bits, aq::moe::Bank* out) {
+    aq_status st;
+    if ((st = check_view(wq, name, 3, 3)) != AQ_OK) return st;
+    if ((st = check_view(sc, name, 3, 3)) != AQ_OK) return st;
+    if ((st = check_view(bi, name, 3, 3)) != AQ_OK) return st;
+    if (wq->dtype != AQ_U32) return fail(AQ_ERR_DTYPE, "%s: codes must be u32", name);
+    if (sc->dtype != dt || bi->dtype != dt) return fail(AQ_ERR_DTYPE, "%s: scales/biases must have x's dtype", name);
+    if (K % group != 0) return fail(AQ_ERR_GROUP, "%s: %lld columns not a multiple of group=%d", name, (long long)K, group);
+    const int64_t kg = K / group;
+    if (wq->shape[0] != E || wq->shape[1] != rows || wq->shape[2] != K * bits / 32)
+        return fail(AQ_ERR_SHAPE, "%s: codes must be [%lld, %lld, %lld]", name, (long long)E, (long long)rows, (long long)(K * bits / 32));
+    for (const aq_view* v : {sc, bi}) {
+        if (v->shape[0] != E || v->shape[1] != rows || v->shape[2] != kg)
+            return fail(AQ_ERR_SHAPE, "%s: scales/biases must be [%lld, %lld, %lld]", name, (long long)E, (long long)rows, (long long)kg);
+        if (rows > 1 && v->stride[1] != kg) return fail(AQ_ERR_UNSUPPORTED, "%s: scale/bias rows must be contiguous", name);
+    }
+    if (numel(wq) > 0 && (!aligned16(wq->data) || (E > 1 && wq->stride[0] % 4 != 0) || (rows > 1 && wq->stride[1] % 4 != 0)))
+        return fail(AQ_ERR_ALIGN, "%s: rows of codes must be 16-byte aligned", name);
+    out->wq = (const uint32_t*)wq->data;
+    out->scales = (const uint16_t*)sc->data;
+    out->biases = (const uint16_t*)bi->data;
+    out->w_row = rows > 1 ? wq->stride[1] : 0;
+    out->w_exp = E > 1 ? wq->stride[0] : 0;
+    out->s_exp = E > 1 ? sc->stride[0] : 0;
+    out->b_exp = E > 1 ? bi->stride[0] : 0;
+    // scales of a 64-byte stage (512 / bits codes) of a row as one load
+    const int64_t per = 512 / bits / group > 0 ? 512 / bits / group : 1;
+    out->svec = kg % per == 0 && (uintptr_t)sc->data % (2 * per) == 0 && (uintptr_t)bi->data % (2 * per) == 0 &&
+                out->s_exp % per == 0 && out->b_exp % per == 0;
+    return AQ_OK;
+}
+
+aq_status check_moe_sizes(int64_t T, int top_k, int64_t N) {
+    if (T > aq::moe::MAX_TOKENS)
+        return fail(AQ_ERR_UNSUPPORTED, "%lld tokens (up to %d; aq_qmm_t_grouped takes more)", (long long)T, aq::moe::MAX_TOKENS);
+    if (top_k < 1 || top_k > aq::moe::MAX_TOPK) return fail(AQ_ERR_UNSUPPORTED, "top_k=%d (1..%d)", top_k, aq::moe::MAX_TOPK);
+    if (N < 0 || N > (1 << 20)) return fail(AQ_ERR_UNSUPPORTED, "experts of %lld rows (up to 2^20)", (long long)N);
+    return AQ_OK;
 }
 
 }  // namespace
@@ -1181,5 +1234,103 @@ AQ_API aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq
     if (e != cudaSuccess) return cuda_fail(e, "device error word");
     e = aq::kv::launch_attention(a, s, (int)D, group, q->dtype == AQ_BF16, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+    return AQ_OK;
+}
+
+AQ_API aq_status aq_moe_swiglu_workspace(int64_t tokens, int top_k, int64_t n, size_t* bytes) {
+    g_msg[0] = 0;
+    if (!bytes) return fail(AQ_ERR_NULL, "bytes is NULL");
+    if (tokens < 0) return fail(AQ_ERR_SHAPE, "tokens < 0");
+    aq_status st = check_moe_sizes(tokens, top_k, n);
+    if (st != AQ_OK) return st;
+    *bytes = aq::moe::workspace_bytes(tokens, top_k, n);
+    return AQ_OK;
+}
+
+AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_k, int norm_topk, const aq_view* wq_gate,
+                               const aq_view* s_gate, const aq_view* b_gate, const aq_view* wq_up, const aq_view* s_up,
+                               const aq_view* b_up, const aq_view* wq_down, const aq_view* s_down, const aq_view* b_down,
+                               int group, int bits, float rms_eps, const aq_view* r, const aq_view* y, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    g_msg[0] = 0;
+    aq_status st;
+    if ((st = check_view(x, "x", 2, 2)) != AQ_OK) return st;
+    if ((st = check_view(logits, "logits", 2, 2)) != AQ_OK) return st;
+    if ((st = check_view(y, "y", 2, 2)) != AQ_OK) return st;
+    if ((st = check_output(y, "y")) != AQ_OK) return st;
+    if ((st = check_bits_group(bits, group)) != AQ_OK) return st;
+    if (!(bits == 2 || bits == 4 || bits == 8) || (bits == 2 && group == 32))
+        return fail(AQ_ERR_UNSUPPORTED, "the layer takes 4- and 8-bit codes, and 2-bit codes in groups of 64 or 128");
+    if (!is_half(x->dtype)) return fail(AQ_ERR_DTYPE, "x must be bf16 or f16");
+    if (!(logits->dtype == AQ_F32 || is_half(logits->dtype))) return fail(AQ_ERR_DTYPE, "logits must be f32, bf16 or f16");
+    if (y->dtype != x->dtype && y->dtype != AQ_F32) return fail(AQ_ERR_DTYPE, "y must have x's dtype or f32");
+    if (!(rms_eps >= 0.0f) || !(rms_eps - rms_eps == 0.0f)) return fail(AQ_ERR_SHAPE, "rms_eps must be finite and >= 0");
+    const int64_t T = x->shape[0], K = x->shape[1], E = logits->shape[1];
+    if (logits->shape[0] != T) return fail(AQ_ERR_SHAPE, "logits must have x's %lld rows", (long long)T);
+    if (y->shape[0] != T || y->shape[1] != K) return fail(AQ_ERR_SHAPE, "y must have x's shape");
+    if (!wq_gate || wq_gate->rank != 3) return check_view(wq_gate, "gate", 3, 3);
+    const int64_t N = wq_gate->shape[1];
+    if ((st = check_moe_sizes(T, top_k, N)) != AQ_OK) return st;
+    if (E < 1 || E > aq::moe::MAX_EXPERTS) return fail(AQ_ERR_UNSUPPORTED, "%lld experts (1..%d)", (long long)E, aq::moe::MAX_EXPERTS);
+    if (top_k > E) return fail(AQ_ERR_SHAPE, "top_k=%d of %lld experts", top_k, (long long)E);
+    if (K > (1 << 20)) return fail(AQ_ERR_UNSUPPORTED, "model size %lld (up to 2^20)", (long long)K);
+    aq::moe::Args a;
+    memset(&a, 0, sizeof a);
+    if ((st = check_bank(wq_gate, s_gate, b_gate, "gate", x->dtype, E, N, K, group, bits, &a.gate)) != AQ_OK) return st;
+    if ((st = check_bank(wq_up, s_up, b_up, "up", x->dtype, E, N, K, group, bits, &a.up)) != AQ_OK) return st;
+    if ((st = check_bank(wq_down, s_down, b_down, "down", x->dtype, E, K, N, group, bits, &a.down)) != AQ_OK) return st;
+    a.gate.svec = a.up.svec = a.gate.svec && a.up.svec;
+    if (r) {
+        if ((st = check_view(r, "r", 2, 2)) != AQ_OK) return st;
+        if (r->dtype != y->dtype) return fail(AQ_ERR_DTYPE, "r must have y's dtype");
+        if (r->shape[0] != T || r->shape[1] != K) return fail(AQ_ERR_SHAPE, "r must have y's shape");
+        if (overlaps(r, y) && !same_view(r, y)) return fail(AQ_ERR_OVERLAP, "r overlaps y (other than being the same view)");
+    }
+    const size_t need = aq::moe::workspace_bytes(T, top_k, N);
+    aq_view ws;
+    memset(&ws, 0, sizeof ws);
+    ws.data = workspace;
+    ws.dtype = AQ_F32;
+    ws.rank = 1;
+    ws.shape[0] = (int64_t)(need / 4);
+    ws.stride[0] = 1;
+    // x is read before the first element of y is written, so y may be x itself
+    if (overlaps(y, x) && !same_view(y, x)) return fail(AQ_ERR_OVERLAP, "y overlaps x (other than being the same view)");
+    const aq_view* ins[10] = {logits, wq_gate, s_gate, b_gate, wq_up, s_up, b_up, wq_down, s_down, b_down};
+    for (const aq_view* v : ins) {
+        if (overlaps(y, v)) return fail(AQ_ERR_OVERLAP, "y overlaps an input");
+        if (overlaps(&ws, v)) return fail(AQ_ERR_OVERLAP, "the workspace overlaps an input");
+    }
+    if (overlaps(&ws, x) || overlaps(&ws, y) || (r && overlaps(&ws, r))) return fail(AQ_ERR_OVERLAP, "the workspace overlaps x, r or y");
+    if (T == 0 || K == 0) return AQ_OK;
+    if (N == 0) return fail(AQ_ERR_SHAPE, "experts without rows");
+    if (!aligned16(x->data) || (T > 1 && x->stride[0] % 8 != 0)) return fail(AQ_ERR_ALIGN, "rows of x must be 16-byte aligned");
+    if (!workspace) return fail(AQ_ERR_NULL, "workspace is NULL");
+    if (workspace_bytes < need) return fail(AQ_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(AQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if ((st = check_device()) != AQ_OK) return st;
+    a.x = (const uint16_t*)x->data;
+    a.x_row = x->stride[0];
+    a.logits = logits->data;
+    a.l_row = logits->stride[0];
+    a.ldt = logits->dtype;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.topk = top_k;
+    a.norm = norm_topk != 0;
+    a.K = (int)K;
+    a.N = (int)N;
+    uint8_t* w = (uint8_t*)workspace;
+    a.h_hi = (uint16_t*)w;
+    a.h_lo = (uint16_t*)(w + aq::moe::h_bytes(T, top_k, N));
+    a.h_sum = (float*)(w + 2 * aq::moe::h_bytes(T, top_k, N));
+    a.y = y->data;
+    a.y_row = y->stride[0];
+    a.ydt = y->dtype;
+    a.r = r ? r->data : nullptr;
+    a.r_row = r ? r->stride[0] : 0;
+    a.rms_eps = rms_eps;
+    cudaError_t e = aq::moe::launch(a, bits, group, x->dtype == AQ_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "mixture-of-experts launch");
     return AQ_OK;
 }

@@ -1,0 +1,14 @@
+// kernels_moe_b8_bf16.cu -- mixture-of-experts kernels for 8-bit codes with bf16 activations
+// (moe_kernel.cuh; one file per instantiation set so that they compile in parallel).
+#include "moe_kernel.cuh"
+
+namespace aq {
+namespace moe {
+
+template <>
+cudaError_t launch_b<8, true>(const Args& a, int group, cudaStream_t s) {
+    return launch_g<8, bf16_t>(a, group, s);
+}
+
+}  // namespace moe
+}  // namespace aq

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -91,16 +92,17 @@ def load_library(path: str = LIB_PATH):
         lib.aq_qmm_t_swiglu.restype = ci
         lib.aq_qmm_t_residual.argtypes = [V, V, V, V, ci, ci, V, V, vp]
         lib.aq_qmm_t_residual.restype = ci
-        lib.aq_kv_append.argtypes = [V, V, vp, ci, ci] + [V] * 8 + [vp]
+        # views by address (_views)
+        lib.aq_kv_append.argtypes = [vp, vp, vp, ci, ci] + [vp] * 8 + [vp]
         lib.aq_kv_append.restype = ci
-        lib.aq_kv_attention_workspace.argtypes = [V, V, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.aq_kv_attention_workspace.argtypes = [vp, vp, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
         lib.aq_kv_attention_workspace.restype = ci
-        lib.aq_kv_attention.argtypes = [V] * 7 + [ci, ci, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, ci, V, vp,
+        lib.aq_kv_attention.argtypes = [vp] * 7 + [ci, ci, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, ci, vp, vp,
                                                   ctypes.c_size_t, vp]
         lib.aq_kv_attention.restype = ci
         lib.aq_moe_swiglu_workspace.argtypes = [ctypes.c_int64, ci, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
         lib.aq_moe_swiglu_workspace.restype = ci
-        lib.aq_moe_swiglu.argtypes = [V, V, ci, ci] + [V] * 9 + [ci, ci, ctypes.c_float, V, V, vp, ctypes.c_size_t, vp]
+        lib.aq_moe_swiglu.argtypes = [vp, vp, ci, ci] + [vp] * 9 + [ci, ci, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
         lib.aq_moe_swiglu.restype = ci
         lib.aq_plan_linear.argtypes = [V, V, V, V, ci, ci, V, ci, ctypes.POINTER(AqPlan)]
         lib.aq_plan_linear.restype = ci
@@ -132,6 +134,56 @@ def view(t: torch.Tensor) -> AqView:
         v.shape[i] = t.shape[i]
         v.stride[i] = t.stride(i)
     return v
+
+
+_PACK = {r: struct.Struct(f"<Qii{r}q{8 * (4 - r)}x{r}q{8 * (4 - r)}x") for r in (1, 2, 3, 4)}   # an AqView of rank r
+_VIEW_BYTES = ctypes.sizeof(AqView)
+_scratch = threading.local()
+
+
+def _views(*tensors) -> list:
+    """Addresses of the views of `tensors` (None for None), packed into this thread's scratch buffer: valid until its next
+    call.  What view() builds, at a fraction of the cost: the calls of a decode step are short."""
+    buf = getattr(_scratch, "buf", None)
+    if buf is None:
+        buf = _scratch.buf = ctypes.create_string_buffer(16 * _VIEW_BYTES)
+        _scratch.base = ctypes.addressof(buf)
+    at, out = 0, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        shape = t.shape
+        rank = len(shape)
+        if rank > 4 or rank < 1:
+            raise ValueError("aq views have rank 1..4")
+        dt = _DT.get(t.dtype)
+        if dt is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        _PACK[rank].pack_into(buf, at, t.data_ptr(), dt, rank, *shape, *t.stride())
+        out.append(_scratch.base + at)
+        at += _VIEW_BYTES
+    return out
+
+
+class _On:
+    """The device of `t` made current for the duration of a call, if it is not, and the raw handle of its current stream."""
+
+    def __init__(self, t: torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        self.dev = t.device.index
+        self.guard = None
+
+    def __enter__(self) -> int:
+        if torch._C._cuda_getDevice() != self.dev:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -295,9 +347,8 @@ def aq_qmv_gathered(x, x_ids, w_ids, wq_bank, s_bank, b_bank, group: int, bits: 
 def _ids(t: torch.Tensor, name: str, dim: int, device):
     if t.dtype != torch.int64 or t.device != device or t.dim() != dim:
         raise TypeError(f"{name} must be a {dim}D int64 tensor on {device}")
-    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise TypeError(f"{name} must be contiguous")
-    return t
 
 
 def aq_kv_append(k, v, slots, k_cache, v_cache, group: int, bits: int, k_out=None, v_out=None):
@@ -306,13 +357,11 @@ def aq_kv_append(k, v, slots, k_cache, v_cache, group: int, bits: int, k_out=Non
     written in place.  k_out, v_out [T, H, D]: the values that the cache then stands for."""
     lib = load_library()
     _ids(slots, "slots", 1, k.device)
-    if slots.numel() != k.shape[0]:
+    if slots.shape[0] != k.shape[0]:
         raise ValueError("one slot per token")
-    with torch.cuda.device(k.device):
-        _check(lib, lib.aq_kv_append(view(k), view(v), ctypes.c_void_p(slots.data_ptr()), group, bits,
-                                     *[view(t) for t in (*k_cache, *v_cache)],
-                                     None if k_out is None else view(k_out), None if v_out is None else view(v_out),
-                                     _stream(k)))
+    with _On(k) as stream:
+        vk, vv, *rest = _views(k, v, *k_cache, *v_cache, k_out, v_out)
+        _check(lib, lib.aq_kv_append(vk, vv, slots.data_ptr(), group, bits, *rest, stream))
 
 
 def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, scale: float | None = None,
@@ -329,16 +378,15 @@ def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, 
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    vq, vk = view(q), view(k_cache[0])
-    need = ctypes.c_size_t()
-    with torch.cuda.device(q.device):
-        stream = _stream(q)
-        _check(lib, lib.aq_kv_attention_workspace(vq, vk, pages.shape[1], ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-        _check(lib, lib.aq_kv_attention(vq, vk, *[view(t) for t in (*k_cache[1:], *v_cache)], group, bits,
-                                        ctypes.c_void_p(pages.data_ptr()), pages.stride(0), pages.shape[1],
-                                        ctypes.c_void_p(lengths.data_ptr()), float(scale), int(window), view(out),
-                                        ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream))
+    max_pages = pages.shape[1]
+    with _On(q) as stream:
+        vq, vk, *rest, vo = _views(q, *k_cache, *v_cache, out)
+        need = ctypes.c_size_t()
+        _check(lib, lib.aq_kv_attention_workspace(vq, vk, max_pages, ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device) if need.value else None
+        _check(lib, lib.aq_kv_attention(vq, vk, *rest, group, bits, pages.data_ptr(), pages.stride(0), max_pages,
+                                        lengths.data_ptr(), scale, window, vo, ws.data_ptr() if need.value else None,
+                                        need.value, stream))
     return out
 
 
@@ -350,15 +398,13 @@ def aq_moe_swiglu(x, logits, top_k: int, gate, up, down, group: int, bits: int, 
     lib = load_library()
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    need = ctypes.c_size_t()
-    with torch.cuda.device(x.device):
-        stream = _stream(x)
+    with _On(x) as stream:
+        need = ctypes.c_size_t()
         _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, gate[0].shape[-2], ctypes.byref(need)))
         ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        _check(lib, lib.aq_moe_swiglu(view(x), view(logits), top_k, 1 if norm_topk else 0,
-                                      *[view(t) for t in (*gate, *up, *down)], group, bits, float(rms_eps),
-                                      None if residual is None else view(residual), view(out),
-                                      ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream))
+        vx, vl, *banks, vr, vy = _views(x, logits, *gate, *up, *down, residual, out)
+        _check(lib, lib.aq_moe_swiglu(vx, vl, top_k, 1 if norm_topk else 0, *banks, group, bits, rms_eps, vr, vy,
+                                      ws.data_ptr(), need.value, stream))
     return out
 
 

@@ -545,8 +545,12 @@ aq_status check_attention_q(const aq_view* q, const aq_view* k_wq, int64_t max_p
     if (D != 64 && D != 128 && D != 256) return fail(AQ_ERR_UNSUPPORTED, "head size %lld (64, 128 and 256 are supported)", (long long)D);
     if (H < 1 || Hq % H != 0) return fail(AQ_ERR_SHAPE, "%lld query heads are not a multiple of %lld key/value heads", (long long)Hq, (long long)H);
     if (max_pages < 0) return fail(AQ_ERR_SHAPE, "max_pages < 0");
-    if (max_pages > 0x7fffffff || S > 0x7fffffff || max_pages * S > 0x7fffffff)
-        return fail(AQ_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens per sequence");
+    if (max_pages > (1 << 30) || S > (1 << 30) || max_pages * S > (1 << 30))
+        return fail(AQ_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+    // work units of 64 tokens, heads and 8 query rows, counted in 32 bits by the kernel
+    if (B <= 65535 && H <= 65535 && Hq / H <= (1 << 20) && Tq <= (1 << 20) &&
+        (double)B * H * (double)(Hq / H * Tq / 8 + 1) * (double)(max_pages * S / 64 + 2) > 2e9)
+        return fail(AQ_ERR_UNSUPPORTED, "more than 2e9 units of 64 tokens and 8 query rows");
     if (B > 65535 || H > 65535 || Hq / H > (1 << 20) || Tq > (1 << 20) || Hq / H * Tq > (1 << 20))
         return fail(AQ_ERR_UNSUPPORTED, "more than 65535 sequences or heads, or 2^20 query rows per key/value head");
     return AQ_OK;
@@ -1226,7 +1230,18 @@ AQ_API aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq
     for (const aq::kv::Side* d : {&a.k, &a.v})
         fast = fast && d->s_slot == kg && d->b_slot == kg && aligned16(d->scales) && aligned16(d->biases) &&
                d->s_page % 8 == 0 && d->s_head % 8 == 0 && d->b_page % 8 == 0 && d->b_head % 8 == 0;
+    // ... and page ids and strides (in bytes) of 32 bits
+    const int64_t lim = 0xffffffffll;
+    fast = fast && a.P < lim;
+    for (const aq::kv::Side* d : {&a.k, &a.v})
+        fast = fast && d->w_page * 4 <= lim && d->w_slot * 4 <= lim && d->s_page * 2 <= lim && d->b_page * 2 <= lim;
+    a.k_page = (uint32_t)(a.k.w_page * 4);
+    a.k_slot = (uint32_t)(a.k.w_slot * 4);
+    a.v_page = (uint32_t)(a.v.w_page * 4);
+    a.v_slot = (uint32_t)(a.v.w_slot * 4);
     a.fast = fast ? 1 : 0;
+    const int unit = aq::kv::unit_tokens((int)D, s.nt);
+    a.unit_slots = S > 0 ? (int)(unit % S) : 0;
     a.split = s.split;
     a.part_o = (float*)workspace;
     a.part_ml = (float*)workspace + s.o_floats;

@@ -16,7 +16,6 @@ extern template cudaError_t launch_d<256, false>(const AttnArgs&, const AttnShap
 
 namespace {
 constexpr int SMS = 148;
-constexpr int UNIT_TOKENS = 64;   // tokens per unit (kv_attention_kernel.cuh)
 }  // namespace
 
 AttnShape attn_shape(int64_t B, int64_t rows, int64_t Hkv, int D, int64_t max_tokens) {
@@ -25,9 +24,15 @@ AttnShape attn_shape(int64_t B, int64_t rows, int64_t Hkv, int D, int64_t max_to
     s.rtiles = (int)((rows + 8 * s.nt - 1) / (8 * s.nt));
     const int64_t items = B * Hkv * s.rtiles;
     // CTAs that fit the device at once (the kernel's launch bounds)
-    const int per_sm = (D == 256 || s.nt == 4) ? 2 : s.nt == 2 ? 3 : 4;
-    const int64_t all = (int64_t)SMS * per_sm;
-    const int64_t most = items * ((max_tokens + UNIT_TOKENS - 1) / UNIT_TOKENS);
+    const int64_t all = (int64_t)SMS * ctas_per_sm(D, s.nt);
+    const int64_t most = items * ((max_tokens + unit_tokens(D, s.nt) - 1) / unit_tokens(D, s.nt));
+    // Short contexts: an item per CTA, which spares the combine launch
+    if (max_tokens <= 512 && items <= 0x7fffffff) {
+        s.split = 0;
+        s.grid = (int)(items < 1 ? 1 : items);
+        s.o_floats = s.ml_floats = 0;
+        return s;
+    }
     s.split = 1;
     s.grid = (int)(most < all ? (most < 1 ? 1 : most) : all);
     s.o_floats = (size_t)2 * s.grid * 8 * s.nt * D;

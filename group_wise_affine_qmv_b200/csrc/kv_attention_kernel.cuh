@@ -14,26 +14,27 @@
 //  - Everything is transposed (S^T = K q^T, O^T = V^T P^T): the 16 rows of mma.sync.m16n8k16 hold
 //    tokens (then V's dims), its 8 columns the query rows of one key/value head.  A tile of 16
 //    tokens x 16 dims is one MMA whatever the number of query heads, up to 8.
-//  - f16 operands whatever q's type: a code widens with one AND-OR into the mantissa of 1024 (low
-//    nibble of a half) or 64 (high nibble), two codes at a time, without shifting each nibble into
-//    place.  For the keys the offsets stay in and leave with the group's fold (O = 1024 sum of even
-//    q + 64 sum of odd q; the fp32 cancellation costs 2^-24 * 1024 / 15 of |s q|, far below the
-//    rounding of p).  For the values they are subtracted (exact): those sums run over the whole
-//    context.  q is scaled by a power of two per row (its largest value near 2^12), so bf16 queries
-//    lose nothing as f16.
+//  - f16 operands whatever q's type: the low byte of a half masked to one nibble is, as it stands, the
+//    f16 subnormal n 2^-24 (low nibble) or n 2^-20 (high nibble), which the tensor cores take exactly.  So
+//    a pair of codes widens with one AND, and half the nibbles need no shift either.  The powers of two
+//    leave with q (keys: its odd dims are scaled by 1/16) and with the final outputs (values).  q itself is
+//    scaled by a power of two per row (its largest value near 2^14), so bf16 queries lose nothing as f16.
 //  - The order of dims inside an MMA is free as long as both operands agree; lanes read whole
 //    words, and q is stored permuted (0,4,1,5,2,6,3,7 within a word).
 //  - V^T needs pairs of tokens in one register: one PRMT per pair of words and half.
 //  - Running maximum: a warp keeps a reference per query row and rescales only when a score exceeds
-//    it by more than 8 (in log2), decided by one vote per 16 tokens: p <= 2^8 instead of 1, and no
+//    it by more than 8 (in log2), decided by one vote per tile: p <= 2^8 instead of 1, and no
 //    shuffles on the usual path.  Sums and the bias term stay per lane until the end.
 //  - p s is rounded to f16 (11 bits, against the output's 8 or 11); s varies over tokens and may
 //    lie anywhere in its 16-bit type's range, so p s is scaled by a power of two per group that
 //    follows the largest |s| seen (the same vote), which keeps p s below 2^15 and exact to 11 bits
 //    down to 2^-29 of that.
 //
-// Work split.  A unit is 64 consecutive tokens of one (sequence, key/value head, row tile), 16 per
-// warp; warps keep their own softmax state and meet only at the end of an item.  All units of all
+//  - A warp's tile is 32 tokens where registers allow it (up to 8 query rows, head size up to 128),
+//    two pieces of 16 whose votes, waits and loop control are shared; else 16.
+//
+// Work split.  A unit is one tile per warp, consecutive tokens of one (sequence, key/value head, row tile);
+// warps keep their own softmax state and meet only at the end of an item.  All units of all
 // items form one line, and every CTA takes an equal stretch of it, so ragged batches and single
 // long sequences load the SMs alike.  A stretch that ends inside an item leaves a partial result
 // (at most two per CTA), which the combine kernel adds in CTA order; nothing depends on timing.
@@ -53,18 +54,11 @@ namespace kv {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-constexpr int TILE = 16;              // tokens per warp and unit
-constexpr int UNIT = TILE * WARPS;
+constexpr int TILE = 16;              // tokens of a piece: the rows of an MMA
 
-// f16 pairs from the nibbles of a word's halves
-__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }   // 1024 + n
-__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w & 0x00F000F0u) | 0x54005400u; }   // 64 + n
-__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t code_lo(uint32_t w) { return hsub2u(nib_lo(w), 0x64006400u); }
-__device__ __forceinline__ uint32_t code_hi(uint32_t w) { return hsub2u(nib_hi(w), 0x54005400u); }
+// f16 pairs from the nibbles of a word's halves: n 2^-24 and n 2^-20
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return w & 0x00F000F0u; }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -83,8 +77,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int size) {   // size 0: zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -95,104 +89,160 @@ __device__ __forceinline__ float2 half_pair(uint32_t v, f16_t) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// N 16-bit values of a row as one load from shared memory
+template <int N, typename XT>
+struct Halves {
+    static constexpr int W = N < 2 ? 1 : N / 2;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        if constexpr (N == 1) w[0] = *p;
+        else if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t*>(p);
+        else if constexpr (N == 4) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+        else *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    }
+    __device__ __forceinline__ float f(int i) const {
+        if constexpr (N == 1) return half_bits_to_float((uint16_t)w[0], XT{});
+        const float2 v = half_pair(w[i >> 1], XT{});
+        return (i & 1) ? v.y : v.x;
+    }
+};
+
 // ---- the line of units ----
 
-// The cached tokens [first, end) that some query of a sequence sees; first on a tile boundary.
+// The cached tokens [first, len) that some query of a sequence sees; first on a tile boundary.
 struct Span {
-    int64_t len, first;
-    int64_t units;
+    int len, first, units;
 };
-__device__ __forceinline__ Span seq_span(const AttnArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int64_t n, int unit) {
     Span s;
-    int64_t n = __ldcg(a.lengths + b);
-    const int64_t most = a.max_pages * a.S;
+    const int most = (int)(a.max_pages * a.S);
     if (n < 0 || n > most) {
         atomicOr(a.err, DEVERR_INDEX);
         n = n < 0 ? 0 : most;
     }
-    s.len = n;
-    int64_t f = 0;
+    s.len = (int)n;
+    s.first = 0;
     if (a.window > 0) {
-        f = n - a.Tq - a.window + 1;
-        f = f < 0 ? 0 : f & ~(int64_t)(TILE - 1);
+        const int64_t f = n - a.Tq - a.window + 1;
+        s.first = f < 0 ? 0 : (int)f & ~(TILE - 1);
     }
-    s.first = f;
-    s.units = (n - f + UNIT - 1) / UNIT;
+    s.units = (s.len - s.first + unit - 1) / unit;
     return s;
 }
 
-__device__ __forceinline__ int64_t warp_incl_scan(int64_t v, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+// The lengths as one warp sees them: 32 sequences at a time, lane b the b-th of the current ones.
+// Every warp of every CTA walks them alike, so nothing has to be shared.
+struct Lengths {
+    const AttnArgs& a;
+    const int lane, unit;
+    int base;              // first sequence held
+    Span mine;
+    __device__ __forceinline__ Lengths(const AttnArgs& args, int ln, int un) : a(args), lane(ln), unit(un), base(-1) { hold(0); }
+    __device__ __forceinline__ void hold(int b0) {
+        if (b0 == base) return;
+        base = b0;
+        mine = span_of(a, b0 + lane < a.B ? __ldcg(a.lengths + b0 + lane) : 0, unit);
+        if (b0 + lane >= a.B) mine.units = 0;
     }
-    return v;
-}
-
-// Units of all sequences, and (second pass) the sequence that holds unit `at` with the units before
-// that sequence.  One warp.  Units count a sequence's items (heads x row tiles) too.
-__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int lane) {
-    int64_t n = 0;
-    for (int b = lane; b < a.B; b += 32) n += seq_span(a, b).units;
-    n *= (int64_t)a.Hkv * a.rtiles;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
-}
-__device__ __forceinline__ void find_seq(const AttnArgs& a, int lane, int64_t at, int* seq, int64_t* before) {
-    const int64_t items = (int64_t)a.Hkv * a.rtiles;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int64_t u = b < a.B ? seq_span(a, b).units * items : 0;
-        const int64_t incl = warp_incl_scan(u, lane) + base;
-        const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            *seq = b0 + l;
-            *before = __shfl_sync(0xffffffffu, incl - u, l);
-            return;
+    __device__ __forceinline__ Span of(int seq) {
+        hold(seq & ~31);
+        Span s;
+        s.len = __shfl_sync(0xffffffffu, mine.len, seq & 31);
+        s.first = __shfl_sync(0xffffffffu, mine.first, seq & 31);
+        s.units = __shfl_sync(0xffffffffu, mine.units, seq & 31);
+        return s;
+    }
+    // units of all sequences, times their items (the host keeps them below 2^31)
+    __device__ __forceinline__ int total() {
+        int n = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            hold(b0);
+            n += mine.units;
         }
-        base = __shfl_sync(0xffffffffu, incl, 31);
+        return __reduce_add_sync(0xffffffffu, n) * a.Hkv * a.rtiles;
     }
-    *seq = a.B;
-    *before = base;
-}
-// CTA i of n takes units [i W / n, (i + 1) W / n)
-__device__ __forceinline__ int64_t cut(int64_t W, int64_t n, int64_t i) { return W / n * i + W % n * i / n; }
-// CTAs that share W units: no more than units
-__device__ __forceinline__ int64_t sharing(int64_t W, int64_t grid) { return W < grid ? (W < 1 ? 1 : W) : grid; }
+    // the sequence that holds unit `at`, and the units before that sequence
+    __device__ __forceinline__ void find(int at, int* seq, int* before) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            hold(b0);
+            const int u = mine.units * a.Hkv * a.rtiles;
+            int incl = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            incl += run;
+            const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                *seq = b0 + l;
+                *before = __shfl_sync(0xffffffffu, incl - u, l);
+                return;
+            }
+            run = __shfl_sync(0xffffffffu, incl, 31);
+        }
+        *seq = a.B;
+        *before = run;
+    }
+    // the units before a sequence
+    __device__ __forceinline__ int before(int seq) {
+        int n = 0;
+        for (int b0 = 0; b0 < seq; b0 += 32) {
+            hold(b0);
+            if (b0 + lane < seq) n += mine.units;
+        }
+        return __reduce_add_sync(0xffffffffu, n) * a.Hkv * a.rtiles;
+    }
+};
+// How CTAs share the line: no more CTAs than units, the first `more` of them one unit more than the others.
+struct Shares {
+    int n, each, more;
+    __device__ __forceinline__ Shares(int W, int grid) {
+        n = W < grid ? (W < 1 ? 1 : W) : grid;
+        each = W / n;
+        more = W - each * n;
+    }
+    __device__ __forceinline__ int start(int cta) const { return cta * each + (cta < more ? cta : more); }
+    __device__ __forceinline__ int owner(int unit) const {
+        const int big = more * (each + 1);
+        return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+    }
+};
 
 template <int D, int G, int NT>
 struct Geo {
     static constexpr int KG = D / G;                       // groups per row
-    static constexpr int ROWB = D / 2;                     // bytes of a row of codes
-    static constexpr int CH = ROWB / 16;                   // its 16-byte pieces
-    static constexpr int CODES = TILE * ROWB;              // a tile of one side
+    static constexpr int CH = D / 32;                      // 16-byte chunks of a row of codes
+    static constexpr int PCS = pieces_of(D, NT);           // pieces of a tile
+    // a piece of one side: chunk by chunk, the 16 tokens of a chunk together.  64 bytes of padding between
+    // chunks put the two chunks that a shared-memory phase touches on different banks, and every lane reads
+    // at one address plus constants
+    static constexpr int CP = TILE * 16 + 64;
+    static constexpr int CODES = CH * CP;
     static constexpr int SB = TILE * KG * 2;               // its scales, or its biases
-    static constexpr int STAGE = 2 * CODES + 4 * SB;
-    static constexpr int NST = D == 256 ? 3 : 4;           // stages of a warp's ring
+    static constexpr int PIECE = 2 * CODES + 4 * SB;       // keys, values, their scales and biases
+    static constexpr int STAGE = PCS * PIECE;
+    static constexpr int NST = D == 64 ? 4 : 3;                       // stages of a warp's ring
     static constexpr int ROWS = 8 * NT;
     static constexpr int QP = D * 2 + 16;                  // bytes of a q row in shared memory
     static constexpr int RING = WARPS * NST * STAGE;
     static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4;   // partial outputs of the warps (over the ring)
     static constexpr int BODY = RING > MERGE ? RING : MERGE;
-    static constexpr int SMEM = BODY + ROWS * QP + KG * ROWS * 8 + ROWS * 4 + 64;
-    // positions of a side's rows in a tile: 16-byte pieces are swizzled by position so that the eight
-    // lanes of a shared-memory phase meet different banks
-    static __device__ __forceinline__ int swz(int pos) {
-        return D == 256 ? (pos & 3) << 1 : D == 128 ? ((pos >> 1) & 1) << 1 : 0;
-    }
-    // token t of a value tile: even tokens of an octet first, then odd ones
+    static constexpr int SMEM = BODY + ROWS * QP + KG * ROWS * 4 + ROWS * 4;
+    // value token t of a piece: even tokens of an octet first, then odd ones
     static __device__ __forceinline__ int vpos(int t) { return (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3); }
+    static __device__ __forceinline__ int vtok(int pos) { return (pos & 8) | ((pos & 3) << 1) | ((pos >> 2) & 1); }
 };
 
-template <int D, int G, int NT, typename XT>
-__global__ void __launch_bounds__(THREADS, (D == 256 || NT == 4) ? 2 : NT == 2 ? 3 : 4)
+template <int D, int G, int NT, typename XT, bool FAST>
+__global__ void __launch_bounds__(THREADS, ctas_per_sm(D, NT))
 attention_kernel(const __grid_constant__ AttnArgs a) {
     using Gm = Geo<D, G, NT>;
-    constexpr int KG = Gm::KG, ROWS = Gm::ROWS, NST = Gm::NST;
+    constexpr int KG = Gm::KG, ROWS = Gm::ROWS, NST = Gm::NST, PCS = Gm::PCS;
+    constexpr int UNIT = unit_tokens(D, NT);
+    static_assert(UNIT == WARPS * PCS * TILE, "a tile per warp");
     constexpr int KS = G < 64 ? G : 64;        // dims per sub-block
     constexpr int SUBS = D / KS;
     constexpr int MT = D / 16;                 // m tiles of the output
@@ -200,169 +250,192 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* qs = smem + Gm::BODY;                                        // [ROWS][QP] f16, permuted
-    float2* xo = reinterpret_cast<float2*>(qs + ROWS * Gm::QP);           // [KG][ROWS] (X, O)
-    float* csc = reinterpret_cast<float*>(xo + KG * ROWS);                // [ROWS] score scale
-    volatile int64_t* sched = reinterpret_cast<volatile int64_t*>(reinterpret_cast<uint8_t*>(csc) + ROWS * 4);
+    float* xs = reinterpret_cast<float*>(qs + ROWS * Gm::QP);             // [KG][ROWS] sums of q
+    float* csc = xs + KG * ROWS;                                          // [ROWS] score scale
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
 
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();   // q and the cache may come from the kernels before
-
-    if (warp == 0) {
-        int64_t lo = 0, hi = 0, before = 0;
-        int seq = 0;
-        if (a.split) {
-            const int64_t W = total_units(a, lane);
-            const int64_t n = sharing(W, gridDim.x);
-            if ((int64_t)blockIdx.x < n) {
-                lo = cut(W, n, blockIdx.x);
-                hi = cut(W, n, (int64_t)blockIdx.x + 1);
-            }
-            if (lo < hi) find_seq(a, lane, lo, &seq, &before);
-        } else {   // one item per CTA
-            const int items = a.Hkv * a.rtiles;
-            seq = blockIdx.x / items;
-            const int64_t units = seq_span(a, seq).units;
-            lo = (blockIdx.x - seq * items) * units;
-            hi = lo + units;
+    ptx::pdl_wait();                 // q, the cache and the lengths may come from the kernels before
+    ptx::pdl_launch_dependents();    // after the wait: the combine kernel reads the lengths before its own
+    Lengths L(a, lane, UNIT);
+    int at = 0, at_end = 0, before = 0, seq = 0;
+    if (a.split) {
+        const Shares sh(L.total(), gridDim.x);
+        if ((int)blockIdx.x < sh.n) {
+            at = sh.start(blockIdx.x);
+            at_end = sh.start(blockIdx.x + 1);
         }
-        if (lane == 0) {
-            sched[0] = lo;
-            sched[1] = hi;
-            sched[2] = seq;
-            sched[3] = before;
-        }
+        if (at < at_end) L.find(at, &seq, &before);
+    } else {   // one item per CTA
+        const int items = a.Hkv * a.rtiles;
+        seq = blockIdx.x / items;
+        const int units = L.of(seq).units;
+        at = ((int)blockIdx.x - seq * items) * units;
+        at_end = at + units;
     }
-    // sequences without a visible token: their rows are zeros
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (seq_span(a, b).units == 0) {
-            const int64_t n = (int64_t)a.Tq * a.Hq * D;
-            for (int64_t i = threadIdx.x; i < n; i += THREADS) {
-                const int64_t th = i / D, t = th / a.Hq;
-                a.out[b * a.o_b + t * a.o_t + (th - t * a.Hq) * a.o_h + (i - th * D)] = 0;
-            }
-        }
-    __syncthreads();
-    int64_t at = sched[0];
-    const int64_t at_end = sched[1];
-    int seq = (int)sched[2];
-    int64_t before = sched[3];
     bool first_seg = true;
 
     uint8_t* ring = smem + warp * NST * Gm::STAGE;
+    // this lane's words of a tile: of token r (keys), of token 2c (values)
+    const int k_lane = KS == 64 ? (c >> 1) * Gm::CP + r * 16 + (c & 1) * 8 : r * 16 + c * 4;
+    const int v_lane = KS == 64 ? (r >> 2) * Gm::CP + c * 16 + (r & 3) * 4 : c * 16 + (r >> 1) * 4;
     const uint32_t ring_s = ptx::smem_u32(ring);
 
     while (at < at_end) {
         // ---- the segment: units [u0, u1) of item (seq, head, row tile) ----
-        Span sp = seq_span(a, seq);
-        const int64_t items = (int64_t)a.Hkv * a.rtiles;
+        Span sp = L.of(seq);
+        const int items = a.Hkv * a.rtiles;
         while (at >= before + sp.units * items) {
             before += sp.units * items;
-            sp = seq_span(a, ++seq);
+            sp = L.of(++seq);
         }
-        const int64_t it = (at - before) / sp.units;
-        const int64_t u0 = at - before - it * sp.units;
-        const int64_t u1 = u0 + (at_end - at) < sp.units ? u0 + (at_end - at) : sp.units;
-        const int head = (int)(it / a.rtiles), rt = (int)(it - (int64_t)head * a.rtiles);
+        const int in_seq = at - before;
+        const int it = in_seq / sp.units;
+        const int u0 = in_seq - it * sp.units;
+        const int u1 = at_end - at < sp.units - u0 ? u0 + at_end - at : sp.units;
+        const int head = it / a.rtiles, rt = it - head * a.rtiles;
         const int row0 = rt * ROWS;
         at += u1 - u0;
         const int64_t* pages = a.pages + seq * a.pages_row;
 
-        // ---- loads of a tile (16 tokens from t0) into ring slot st ----
-        auto load_tile = [&](int64_t t0, int st) {
-            const uint32_t dst = ring_s + st * Gm::STAGE;
-            if (a.fast) {
-                const int64_t pg = t0 / a.S;
-                const int64_t sl = t0 - pg * a.S;
-                const int64_t pid = __ldcg(pages + pg);
-                if (pid < 0 || pid >= a.P) {   // no such page: its tokens take no part (zero scales)
-                    if (lane == 0) atomicOr(a.err, DEVERR_INDEX);
-                    return false;
-                }
-                const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.k.wq + pid * a.k.w_page + head * a.k.w_head + sl * a.k.w_slot);
-                const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v.wq + pid * a.v.w_page + head * a.v.w_head + sl * a.v.w_slot);
-#pragma unroll
-                for (int i = 0; i < TILE * Gm::CH / 32; ++i) {
-                    const int x = lane + 32 * i, row = x / Gm::CH, ch = x % Gm::CH;
-                    cp16(dst + row * Gm::ROWB + ((ch ^ Gm::swz(row)) << 4), kp + row * a.k.w_slot * 4 + ch * 16);
-                    const int vp_ = Gm::vpos(row);
-                    cp16(dst + Gm::CODES + vp_ * Gm::ROWB + ((ch ^ Gm::swz(vp_)) << 4), vp + row * a.v.w_slot * 4 + ch * 16);
-                }
-                // scales and biases: 16 tokens are one run of 2 KG pieces per array
-#pragma unroll
-                for (int i = 0; i < (8 * KG + 31) / 32; ++i) {
-                    const int x = lane + 32 * i;
-                    if (x < 8 * KG) {
-                        const int arr = x / (2 * KG), ch = x % (2 * KG);
-                        const Side& sd = arr < 2 ? a.k : a.v;
-                        const uint16_t* p = (arr & 1) ? sd.biases + pid * sd.b_page + head * sd.b_head + sl * sd.b_slot
-                                                      : sd.scales + pid * sd.s_page + head * sd.s_head + sl * sd.s_slot;
-                        cp16(dst + 2 * Gm::CODES + arr * Gm::SB + ch * 16, p + ch * 8);
-                    }
-                }
-                return true;
-            }
-            // any page size and strides: rows one by one, scales through registers
-            bool ok = true;
-            for (int x = lane; x < TILE * Gm::CH; x += 32) {
-                const int row = x / Gm::CH, ch = x % Gm::CH;
-                const int64_t t = t0 + row;
-                if (t >= sp.len) continue;
-                const int64_t pg = t / a.S, sl = t - pg * a.S;
-                const int64_t pid = __ldcg(pages + pg);
-                if (pid < 0 || pid >= a.P) {
-                    atomicOr(a.err, DEVERR_INDEX);
-                    ok = false;
-                    continue;
-                }
-                const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.k.wq + pid * a.k.w_page + head * a.k.w_head + sl * a.k.w_slot);
-                const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v.wq + pid * a.v.w_page + head * a.v.w_head + sl * a.v.w_slot);
-                cp16(dst + row * Gm::ROWB + ((ch ^ Gm::swz(row)) << 4), kp + ch * 16);
-                const int vp_ = Gm::vpos(row);
-                cp16(dst + Gm::CODES + vp_ * Gm::ROWB + ((ch ^ Gm::swz(vp_)) << 4), vp + ch * 16);
-            }
-            uint16_t* sc = reinterpret_cast<uint16_t*>(ring + st * Gm::STAGE + 2 * Gm::CODES);
-            for (int x = lane; x < TILE * KG; x += 32) {
-                const int row = x / KG, g = x % KG;
-                const int64_t t = t0 + row;
-                uint16_t v4[4] = {0, 0, 0, 0};
-                if (t < sp.len) {
-                    const int64_t pg = t / a.S, sl = t - pg * a.S;
-                    const int64_t pid = __ldcg(pages + pg);
-                    if (pid >= 0 && pid < a.P) {
-                        v4[0] = __ldcg(a.k.scales + pid * a.k.s_page + head * a.k.s_head + sl * a.k.s_slot + g);
-                        v4[1] = __ldcg(a.k.biases + pid * a.k.b_page + head * a.k.b_head + sl * a.k.b_slot + g);
-                        v4[2] = __ldcg(a.v.scales + pid * a.v.s_page + head * a.v.s_head + sl * a.v.s_slot + g);
-                        v4[3] = __ldcg(a.v.biases + pid * a.v.b_page + head * a.v.b_head + sl * a.v.b_slot + g);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sc[k * TILE * KG + x] = v4[k];
-            }
-            return (bool)__all_sync(0xffffffffu, ok);
-        };
-        const int nu = (int)(u1 - u0);
-        const int64_t tw = sp.first + u0 * UNIT + warp * TILE;     // this warp's tile of unit u0
-        // tiles of this warp with a token below len
-        int nt = 0;
+        // ---- this warp's tiles: 16 PCS tokens from tw, every UNIT ----
+        const int nu = u1 - u0;
+        const int tw = sp.first + u0 * UNIT + warp * (PCS * TILE);
+        int nt = 0;                  // those with a token below len
         if (tw < sp.len) {
-            const int64_t left = (sp.len - tw + UNIT - 1) / UNIT;
-            nt = left < nu ? (int)left : nu;
+            const int left = (sp.len - tw + UNIT - 1) / UNIT;
+            nt = left < nu ? left : nu;
         }
-        unsigned bad = 0;   // ring slots whose page does not exist (uniform in the warp)
-        auto issue = [&](int i) {
-            const int st = i % NST;
+        bool missing = false;        // a page id outside the cache: its tokens count as zeros
+
+        // Fast layout: a piece lies in one page, and a lane copies the same chunks of every piece.  The
+        // slot in the page moves on by whole units.  Page ids are fetched 32 tiles at a time, a lane per
+        // tile, one batch ahead, so that no copy waits for one.  All strides fit 32 bits (in bytes).
+        int l_slot = 0;
+        uint32_t pid_now[PCS];       // this lane's tile of the current batch; ~0: no such page
+        int64_t pid_next[PCS];       // ... of the next one, as loaded: a look at one would wait for it
+        const uint8_t *kh = nullptr, *vh = nullptr, *sh = nullptr;
+        uint32_t s_page = 0;
+        // this lane's chunk and tokens: eight lanes write one stretch of banks, a warp reads whole rows
+        const int l_ch = (lane & 1) | (Gm::CH >= 4 ? ((lane >> 3) & (Gm::CH / 2 - 1)) << 1 : 0);
+        const int l_row = ((lane >> 1) & 3) | (Gm::CH == 2 ? (lane >> 3) << 2 : Gm::CH == 4 ? (lane >> 4) << 2 : 0);
+        constexpr int RPI = 32 / Gm::CH;             // tokens per copy instruction
+        auto fetch_pids = [&](int i0) {              // the pages of tiles i0 .. i0 + 31
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc) {
+                pid_next[pc] = -1;
+                if (i0 + lane < nt) {
+                    const int t = tw + (i0 + lane) * UNIT + pc * TILE;
+                    if (t < sp.len) pid_next[pc] = __ldcg(pages + t / a.S);
+                }
+            }
+        };
+        auto next_pids = [&](int i0) {               // the fetched batch becomes the current one, tiles i0 .. on
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc) pid_now[pc] = (uint64_t)pid_next[pc] < (uint64_t)a.P ? (uint32_t)pid_next[pc] : 0xffffffffu;
+            fetch_pids(i0 + 32);
+        };
+        if constexpr (FAST) {
+            l_slot = tw % a.S;
+            fetch_pids(0);
+            kh = reinterpret_cast<const uint8_t*>(a.k.wq + head * a.k.w_head + l_row * a.k.w_slot) + l_ch * 16;
+            vh = reinterpret_cast<const uint8_t*>(a.v.wq + head * a.v.w_head + Gm::vtok(l_row) * a.v.w_slot) + l_ch * 16;
+            // scales and biases: a piece is one run of 2 KG chunks in each of the four arrays; with KG 8
+            // this lane copies chunk lane % 16 of two arrays (keys' and values', lane / 16 choosing)
+            const int arr = (lane / (2 * KG)) & 3, pc = lane % (2 * KG);
+            const Side& sd = arr < 2 ? a.k : a.v;
+            const bool bias = arr & 1;
+            sh = reinterpret_cast<const uint8_t*>((bias ? sd.biases + head * sd.b_head : sd.scales + head * sd.s_head) + pc * 8);
+            s_page = (uint32_t)((bias ? sd.b_page : sd.s_page) * 2);
+        }
+        auto load_fast = [&](int i, uint32_t dst) {
+            const int t0 = tw + i * UNIT;
+            if ((i & 31) == 0) next_pids(i);
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc)
+                if (t0 + pc * TILE < sp.len) {
+                    const uint32_t id = __shfl_sync(0xffffffffu, pid_now[pc], i & 31);
+                    const bool ok = id != 0xffffffffu;
+                    const uint32_t pid = ok ? id : 0u;
+                    const int size = ok ? 16 : 0;    // zeros for a missing page
+                    uint32_t slot = l_slot + pc * TILE;
+                    if (slot >= (uint32_t)a.S) slot = 0;
+                    missing |= !ok;
+                    const uint32_t d0 = dst + pc * Gm::PIECE;
+                    const uint8_t* kp = kh + (uint64_t)pid * a.k_page + (uint64_t)slot * a.k_slot;
+                    const uint8_t* vp = vh + (uint64_t)pid * a.v_page + (uint64_t)slot * a.v_slot;
+#pragma unroll
+                    for (int i = 0; i < TILE / RPI; ++i) {
+                        // D 256 copies four tokens at a time: values in the order of their positions
+                        const int vt = Gm::CH == 8 ? (i & 1) + 8 * (i >> 1) : RPI * i;
+                        cp16(d0 + l_ch * Gm::CP + (l_row + RPI * i) * 16, kp + (uint64_t)(RPI * i) * a.k_slot, size);
+                        cp16(d0 + Gm::CODES + l_ch * Gm::CP + (l_row + RPI * i) * 16, vp + (uint64_t)vt * a.v_slot, size);
+                    }
+                    const uint8_t* sp_ = sh + (uint64_t)pid * s_page + slot * (KG * 2);
+                    if (KG >= 4 || lane < 8 * KG) cp16(d0 + 2 * Gm::CODES + lane * 16, sp_, size);
+                    if constexpr (KG == 8) {         // the values' two arrays
+                        const bool bias = lane >= 16;
+                        const uint8_t* vs = reinterpret_cast<const uint8_t*>(
+                            bias ? a.v.biases + pid * a.v.b_page + head * a.v.b_head : a.v.scales + pid * a.v.s_page + head * a.v.s_head);
+                        cp16(d0 + 2 * Gm::CODES + 512 + lane * 16, vs + slot * (KG * 2) + (lane & 15) * 16, size);
+                    }
+                }
+            l_slot += a.unit_slots;
+            if (l_slot >= a.S) l_slot -= a.S;
+        };
+        // any page size and strides: rows one by one, scales through registers
+        auto load_any = [&](int t00, int st) {
+#pragma unroll 1
+            for (int pc = 0; pc < PCS; ++pc) {
+                const int t0 = t00 + pc * TILE;
+                const uint32_t dst = ring_s + st * Gm::STAGE + pc * Gm::PIECE;
+                for (int x = lane; x < TILE * Gm::CH; x += 32) {
+                    const int row = x / Gm::CH, ch = x % Gm::CH;
+                    const int t = t0 + row;
+                    if (t >= sp.len) continue;
+                    const int pg = t / a.S, sl = t - pg * a.S;
+                    int64_t pid = __ldcg(pages + pg);
+                    const bool ok = (uint64_t)pid < (uint64_t)a.P;
+                    missing |= !ok;
+                    if (!ok) pid = 0;
+                    const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.k.wq + pid * a.k.w_page + head * a.k.w_head + sl * a.k.w_slot);
+                    const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v.wq + pid * a.v.w_page + head * a.v.w_head + sl * a.v.w_slot);
+                    cp16(dst + ch * Gm::CP + row * 16, kp + ch * 16, ok ? 16 : 0);
+                    cp16(dst + Gm::CODES + ch * Gm::CP + Gm::vpos(row) * 16, vp + ch * 16, ok ? 16 : 0);
+                }
+                uint16_t* sc = reinterpret_cast<uint16_t*>(ring + st * Gm::STAGE + pc * Gm::PIECE + 2 * Gm::CODES);
+                for (int x = lane; x < TILE * KG; x += 32) {
+                    const int row = x / KG, g = x % KG;
+                    const int t = t0 + row;
+                    uint16_t v4[4] = {0, 0, 0, 0};
+                    if (t < sp.len) {
+                        const int pg = t / a.S, sl = t - pg * a.S;
+                        const int64_t pid = __ldcg(pages + pg);
+                        if ((uint64_t)pid < (uint64_t)a.P) {
+                            v4[0] = __ldcg(a.k.scales + pid * a.k.s_page + head * a.k.s_head + sl * a.k.s_slot + g);
+                            v4[1] = __ldcg(a.k.biases + pid * a.k.b_page + head * a.k.b_head + sl * a.k.b_slot + g);
+                            v4[2] = __ldcg(a.v.scales + pid * a.v.s_page + head * a.v.s_head + sl * a.v.s_slot + g);
+                            v4[3] = __ldcg(a.v.biases + pid * a.v.b_page + head * a.v.b_head + sl * a.v.b_slot + g);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[k * TILE * KG + x] = v4[k];
+                }
+            }
+        };
+        auto issue = [&](int i, int st) {
             if (i < nt) {
-                if (load_tile(tw + (int64_t)i * UNIT, st)) bad &= ~(1u << st);
-                else bad |= 1u << st;
+                if constexpr (FAST) load_fast(i, ring_s + st * Gm::STAGE);
+                else load_any(tw + i * UNIT, st);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
-        for (int i = 0; i < NST - 1; ++i) issue(i);
+        for (int i = 0; i < NST - 1; ++i) issue(i, i);
 
-        // ---- q rows of the item: scaled to f16, permuted, with their group sums ----
+        // ---- q rows of the item: scaled to f16, permuted, with their group sums.  The softmax scale's sign
+        // goes with q, so that a row's score scale is positive (a zero scale: q = 0, scale 1) ----
+        const float sgn = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
         for (int row = warp; row < ROWS; row += WARPS) {
             constexpr int EPL = D / 32;           // elements per lane
             const int rr = row0 + row;
@@ -373,36 +446,34 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                 const int i = rr / a.rep;
                 const uint16_t* qp = a.q + seq * a.q_b + i * a.q_t + (head * a.rep + rr - i * a.rep) * (int64_t)a.q_h + lane * EPL;
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) f[e] = half_bits_to_float(__ldcg(qp + e), XT{});
+                for (int e = 0; e < EPL; ++e) f[e] = half_bits_to_float(__ldcg(qp + e), XT{}) * sgn;
             }
             float am = 0.0f;
 #pragma unroll
             for (int e = 0; e < EPL; ++e) am = fmaxf(am, fabsf(f[e]));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            // 2^(12 - exponent of the largest value): exact products (an exponent of infinity stays in range)
+            // 2^(14 - exponent of the largest value): exact products (an exponent of infinity stays in range)
             const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255) - 127, -100), 127);
-            const float up = __uint_as_float((uint32_t)(12 - ex + 127) << 23);
-            float X = 0.0f, O = 0.0f;
+            const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+            float X = 0.0f;
 #pragma unroll
             for (int e = 0; e < EPL; ++e) {
-                const __half hf = __float2half_rn(f[e] * up);
-                const float v = __half2float(hf);
                 const int d = lane * EPL + e, n = d & 7;
-                X += v;
-                O += (n & 1) ? 64.0f * v : 1024.0f * v;
+                X += f[e] * up;
+                // odd dims meet codes of 16 times the weight
+                const __half hf = __float2half_rn((n & 1) ? f[e] * up * 0.0625f : f[e] * up);
                 // order within a word: 0 4 1 5 2 6 3 7
                 const int pos = (d & ~7) + 2 * (n & 3) + (n >> 2);
                 *reinterpret_cast<__half*>(qs + row * Gm::QP + pos * 2) = hf;
             }
             constexpr int GL = G / EPL;           // lanes per group
 #pragma unroll
-            for (int o = GL / 2; o > 0; o >>= 1) {
-                X += __shfl_xor_sync(0xffffffffu, X, o);
-                O += __shfl_xor_sync(0xffffffffu, O, o);
-            }
-            if (lane % GL == 0) xo[(lane / GL) * ROWS + row] = make_float2(X, O);
-            if (lane == 0) csc[row] = a.scale_log2 * __uint_as_float((uint32_t)(ex - 12 + 127) << 23);
+            for (int o = GL / 2; o > 0; o >>= 1) X += __shfl_xor_sync(0xffffffffu, X, o);
+            // scores are kept in units of 2^-24: the codes' weight
+            if (lane % GL == 0) xs[(lane / GL) * ROWS + row] = X * 0x1p-24f;
+            if (lane == 0)
+                csc[row] = (a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2)) * __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * 0x1p24f;
         }
         __syncthreads();
 
@@ -423,14 +494,14 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
         }
 
         // ---- softmax state of this warp ----
-        float mu[NT][2], thr[NT][2], l[NT][2], ab[KG][NT][2], vmul[KG], vthr[KG];
+        float nm[NT][2], thr[NT][2], l[NT][2], ab[KG][NT][2], vmul[KG], vthr[KG];
         float acc[MT][NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mu[n][e] = 0.0f;
-                thr[n][e] = -INFINITY;
+                nm[n][e] = 0.0f;                  // minus the reference, in log2
+                thr[n][e] = -INFINITY;            // the score above which it has to move
                 l[n][e] = 0.0f;
 #pragma unroll
                 for (int g = 0; g < KG; ++g) ab[g][n][e] = 0.0f;
@@ -447,157 +518,178 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.0f;
 
-        const int64_t pos0 = sp.len - a.Tq;       // position of query token 0
+        const int pos0 = sp.len - a.Tq;           // position of query token 0
         const int last_i = a.Tq - 1;
+        int st = 0;                               // ring slot of tile i
 
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
-            issue(i + NST - 1);
+            issue(i + NST - 1, st == 0 ? NST - 1 : st - 1);
             cp_wait<NST - 1>();
             __syncwarp();
-            const int st = i % NST;
             const uint8_t* kt = ring + st * Gm::STAGE;
-            const uint8_t* vt = kt + Gm::CODES;
-            const uint16_t* ssb = reinterpret_cast<const uint16_t*>(kt + 2 * Gm::CODES);
-            const int64_t t0 = tw + (int64_t)i * UNIT;
-            const bool slot_bad = (bad >> st) & 1u;
+            const int t0 = tw + i * UNIT;
             // every token of the tile visible to every row?
-            const bool full = !slot_bad && pos0 >= 0 && t0 + TILE - 1 <= pos0 &&
-                              (a.window == 0 || t0 > pos0 + last_i - a.window);
+            const bool full = pos0 >= 0 && t0 + PCS * TILE - 1 <= pos0 &&
+                              (a.window == 0 || t0 > (int64_t)pos0 + last_i - a.window);
 
-            // ---- scores of tokens r and r + 8 for query rows 2c, 2c + 1 of each n tile ----
-            float s[NT][4];
+            // ---- scores of tokens r and r + 8 of each piece for query rows 2c, 2c + 1 of each n tile ----
+            float s[PCS][NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-            float d[NT][4];
-#pragma unroll
-            for (int sb = 0; sb < SUBS; ++sb) {
-                constexpr int SPG = G / KS;
-                const int g = sb / SPG;
-                if (sb % SPG == 0)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-                uint32_t w0[2], w1[2];            // rows r and r + 8
-                if constexpr (KS == 64) {
-                    const int ch = sb * 2 + (c >> 1), o = (c & 1) * 8;
-                    const uint2 x = *reinterpret_cast<const uint2*>(kt + r * Gm::ROWB + ((ch ^ Gm::swz(r)) << 4) + o);
-                    const uint2 y = *reinterpret_cast<const uint2*>(kt + (r + 8) * Gm::ROWB + ((ch ^ Gm::swz(r + 8)) << 4) + o);
-                    w0[0] = x.x; w0[1] = x.y;
-                    w1[0] = y.x; w1[1] = y.y;
-                } else {
-                    w0[0] = *reinterpret_cast<const uint32_t*>(kt + r * Gm::ROWB + ((sb ^ Gm::swz(r)) << 4) + c * 4);
-                    w1[0] = *reinterpret_cast<const uint32_t*>(kt + (r + 8) * Gm::ROWB + ((sb ^ Gm::swz(r + 8)) << 4) + c * 4);
-                }
-#pragma unroll
-                for (int j = 0; j < KS / 32; ++j) {
-                    const int word = KS == 64 ? sb * 8 + 2 * c + j : sb * 4 + c;
-                    const uint32_t u = w0[j], v = w1[j], us = u >> 8, vs = v >> 8;
-                    const uint32_t e0 = nib_lo(u), e1 = nib_lo(v), e2 = nib_hi(u), e3 = nib_hi(v);
-                    const uint32_t f0 = nib_lo(us), f1 = nib_lo(vs), f2 = nib_hi(us), f3 = nib_hi(vs);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t b[4];
-                        if constexpr (QREG) {
-                            const int w = sb * (KS / 32) + j;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) b[k] = qf[4 * w + k];
-                        } else {
-                            const uint4 x = *reinterpret_cast<const uint4*>(qs + (8 * n + r) * Gm::QP + word * 16);
-                            b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
-                        }
-                        mma_f16(d[n], e0, e1, e2, e3, b[0], b[1]);
-                        mma_f16(d[n], f0, f1, f2, f3, b[2], b[3]);
-                    }
-                }
-                if (sb % SPG == SPG - 1) {        // the group's fold: s (D - O) + b X
-                    const float s0 = half_bits_to_float(ssb[r * KG + g], XT{});
-                    const float s1 = half_bits_to_float(ssb[(r + 8) * KG + g], XT{});
-                    const float b0 = half_bits_to_float(ssb[TILE * KG + r * KG + g], XT{});
-                    const float b1 = half_bits_to_float(ssb[TILE * KG + (r + 8) * KG + g], XT{});
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float4 x = *reinterpret_cast<const float4*>(xo + g * ROWS + 8 * n + 2 * c);
-                        s[n][0] += fmaf(s0, d[n][0] - x.y, b0 * x.x);
-                        s[n][1] += fmaf(s0, d[n][1] - x.w, b0 * x.z);
-                        s[n][2] += fmaf(s1, d[n][2] - x.y, b1 * x.x);
-                        s[n][3] += fmaf(s1, d[n][3] - x.w, b1 * x.z);
-                    }
-                }
-            }
-            float sv[KG][2], bv[KG][2];           // value scales and biases of tokens r and r + 8
-#pragma unroll
-            for (int g = 0; g < KG; ++g) {
-                sv[g][0] = half_bits_to_float(ssb[2 * TILE * KG + r * KG + g], XT{});
-                sv[g][1] = half_bits_to_float(ssb[2 * TILE * KG + (r + 8) * KG + g], XT{});
-                bv[g][0] = half_bits_to_float(ssb[3 * TILE * KG + r * KG + g], XT{});
-                bv[g][1] = half_bits_to_float(ssb[3 * TILE * KG + (r + 8) * KG + g], XT{});
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] *= cs[n][e & 1];
-            if (!full) {
-                // rows see tokens up to their position, and from their window's start; a token that no
-                // row sees (stale, another sequence's, of a missing page) may hold any scale: it is zeroed
-                const int64_t ta = t0 + r, tb = ta + 8;
-                const bool in[2] = {!slot_bad && ta < sp.len && ta >= 0, !slot_bad && tb < sp.len};
+            for (int pc = 0; pc < PCS; ++pc) {
+                const uint8_t* kp = kt + pc * Gm::PIECE;
+                const uint16_t* ssb = reinterpret_cast<const uint16_t*>(kp + 2 * Gm::CODES);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = row0 + 8 * n + 2 * c + (e & 1);
-                        int qi = row / a.rep;
-                        if (qi > last_i) qi = last_i;
-                        const int64_t pos = pos0 + qi, t = e < 2 ? ta : tb;
-                        if (!(in[e >> 1] && t <= pos && (a.window == 0 || t > pos - a.window))) s[n][e] = -INFINITY;
-                    }
-                const int64_t seen_lo = a.window == 0 ? 0 : pos0 - a.window + 1;
+                    for (int e = 0; e < 4; ++e) s[pc][n][e] = 0.0f;
+                float d[NT][4];
+                Halves<KG, XT> ks[2], kb[2];      // key scales and biases of tokens r and r + 8
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    if (!in[0] || ta < seen_lo) sv[g][0] = bv[g][0] = 0.0f;
-                    if (!in[1] || tb < seen_lo) sv[g][1] = bv[g][1] = 0.0f;
+                for (int h = 0; h < 2; ++h) {
+                    ks[h].load(ssb + (r + 8 * h) * KG);
+                    kb[h].load(ssb + TILE * KG + (r + 8 * h) * KG);
                 }
+#pragma unroll
+                for (int sb = 0; sb < SUBS; ++sb) {
+                    constexpr int SPG = G / KS;
+                    const int g = sb / SPG;
+                    if (sb % SPG == 0)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+                    uint32_t w0[2], w1[2];        // rows r and r + 8
+                    if constexpr (KS == 64) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(kp + k_lane + sb * 2 * Gm::CP);
+                        const uint2 y = *reinterpret_cast<const uint2*>(kp + k_lane + sb * 2 * Gm::CP + 8 * 16);
+                        w0[0] = x.x; w0[1] = x.y;
+                        w1[0] = y.x; w1[1] = y.y;
+                    } else {
+                        w0[0] = *reinterpret_cast<const uint32_t*>(kp + k_lane + sb * Gm::CP);
+                        w1[0] = *reinterpret_cast<const uint32_t*>(kp + k_lane + sb * Gm::CP + 8 * 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < KS / 32; ++j) {
+                        const int word = KS == 64 ? sb * 8 + 2 * c + j : sb * 4 + c;
+                        const uint32_t u = w0[j], v = w1[j], us = u >> 8, vs = v >> 8;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t b[4];
+                            if constexpr (QREG) {
+                                const int w = sb * (KS / 32) + j;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) b[k] = qf[4 * w + k];
+                            } else {
+                                const uint4 x = *reinterpret_cast<const uint4*>(qs + (8 * n + r) * Gm::QP + word * 16);
+                                b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+                            }
+                            mma_f16(d[n], nib_lo(u), nib_lo(v), nib_hi(u), nib_hi(v), b[0], b[1]);
+                            mma_f16(d[n], nib_lo(us), nib_lo(vs), nib_hi(us), nib_hi(vs), b[2], b[3]);
+                        }
+                    }
+                    if (sb % SPG == SPG - 1) {    // the group's fold: s D + b X
+                        const float s0 = ks[0].f(g), s1 = ks[1].f(g), b0 = kb[0].f(g), b1 = kb[1].f(g);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float2 x = *reinterpret_cast<const float2*>(xs + g * ROWS + 8 * n + 2 * c);
+                            s[pc][n][0] = fmaf(s0, d[n][0], fmaf(b0, x.x, s[pc][n][0]));
+                            s[pc][n][1] = fmaf(s0, d[n][1], fmaf(b0, x.y, s[pc][n][1]));
+                            s[pc][n][2] = fmaf(s1, d[n][2], fmaf(b1, x.x, s[pc][n][2]));
+                            s[pc][n][3] = fmaf(s1, d[n][3], fmaf(b1, x.y, s[pc][n][3]));
+                        }
+                    }
+                }
+            }
+            float sv[PCS][KG][2], bv[PCS][KG][2]; // value scales and biases of tokens r and r + 8
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc) {
+                const uint16_t* ssb = reinterpret_cast<const uint16_t*>(kt + pc * Gm::PIECE + 2 * Gm::CODES);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    Halves<KG, XT> x, y;
+                    x.load(ssb + 2 * TILE * KG + (r + 8 * h) * KG);
+                    y.load(ssb + 3 * TILE * KG + (r + 8 * h) * KG);
+#pragma unroll
+                    for (int g = 0; g < KG; ++g) {
+                        sv[pc][g][h] = x.f(g);
+                        bv[pc][g][h] = y.f(g);
+                    }
+                }
+            }
+            if (!full) {
+                // rows see tokens up to their position, and from their window's start; a token that no
+                // row sees (stale, another sequence's) may hold any scale: it is zeroed
+                const int64_t seen_lo = a.window == 0 ? 0 : (int64_t)pos0 - a.window + 1;
+#pragma unroll
+                for (int pc = 0; pc < PCS; ++pc)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = t0 + pc * TILE + r + 8 * h;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int row = row0 + 8 * n + 2 * c + e;
+                                int qi = row / a.rep;
+                                if (qi > last_i) qi = last_i;
+                                const int pos = pos0 + qi;
+                                if (!(t <= pos && (a.window == 0 || t > (int64_t)pos - a.window))) s[pc][n][2 * h + e] = -INFINITY;
+                            }
+                        if (t >= sp.len || t < seen_lo)
+#pragma unroll
+                            for (int g = 0; g < KG; ++g) sv[pc][g][h] = bv[pc][g][h] = 0.0f;
+                    }
             }
             // ---- one vote: does a score or a value scale leave the range of the references? ----
             bool out_of = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int pc = 0; pc < PCS; ++pc) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out_of |= s[n][e] > thr[n][e & 1];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int g = 0; g < KG; ++g) out_of |= fmaxf(fabsf(sv[g][0]), fabsf(sv[g][1])) > vthr[g];
+                    for (int e = 0; e < 2; ++e) out_of |= fmaxf(s[pc][n][e], s[pc][n][e + 2]) > thr[n][e];
+            }
+#pragma unroll
+            for (int g = 0; g < KG; ++g) {
+                float m = fmaxf(fabsf(sv[0][g][0]), fabsf(sv[0][g][1]));
+#pragma unroll
+                for (int pc = 1; pc < PCS; ++pc) m = fmaxf(m, fmaxf(fabsf(sv[pc][g][0]), fabsf(sv[pc][g][1])));
+                out_of |= m > vthr[g];
+            }
             if (__any_sync(0xffffffffu, out_of)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(s[n][e], s[n][e + 2]);
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int pc = 0; pc < PCS; ++pc) m = fmaxf(m, fmaxf(s[pc][n][e], s[pc][n][e + 2]));
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if (m > mu[n][e] || thr[n][e] == -INFINITY) {
-                            if (m > -INFINITY) {
-                                const float f = thr[n][e] == -INFINITY ? 0.0f : ex2(mu[n][e] - m);
-                                mu[n][e] = m;
-                                thr[n][e] = m + 8.0f;
-                                l[n][e] *= f;
+                        const bool none = thr[n][e] == -INFINITY;
+                        if (m > -INFINITY && (none || fmaf(m, cs[n][e], nm[n][e]) > 0.0f)) {
+                            const float f = none ? 0.0f : ex2(-fmaf(m, cs[n][e], nm[n][e]));
+                            nm[n][e] = -m * cs[n][e];
+                            thr[n][e] = m + 8.0f / cs[n][e];
+                            l[n][e] *= f;
 #pragma unroll
-                                for (int g = 0; g < KG; ++g) ab[g][n][e] *= f;
+                            for (int g = 0; g < KG; ++g) ab[g][n][e] *= f;
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) {
-                                    acc[mt][n][e] *= f;
-                                    acc[mt][n][e + 2] *= f;
-                                }
+                            for (int mt = 0; mt < MT; ++mt) {
+                                acc[mt][n][e] *= f;
+                                acc[mt][n][e + 2] *= f;
                             }
                         }
                     }
 #pragma unroll
                 for (int g = 0; g < KG; ++g) {
                     // an infinite scale is no reference: it would flush the rows that do not see its token
-                    float m = fmaxf(isinf(sv[g][0]) ? 0.0f : fabsf(sv[g][0]), isinf(sv[g][1]) ? 0.0f : fabsf(sv[g][1]));
+                    float m = 0.0f;
+#pragma unroll
+                    for (int pc = 0; pc < PCS; ++pc)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) m = fmaxf(m, isinf(sv[pc][g][h]) ? 0.0f : fabsf(sv[pc][g][h]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     if (m > vthr[g]) {            // 2^E >= m: p s 2^(6 - E) <= 2^15 until the next change
@@ -615,74 +707,75 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                     }
                 }
             }
-            // ---- p, its sums, and p s as f16 with tokens along k ----
-            uint32_t pb[KG][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float p[4];
+            for (int pc = 0; pc < PCS; ++pc) {
+                // ---- p, its sums, and p s as f16 with tokens along k ----
+                uint32_t pb[KG][NT][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2(s[n][e] - mu[n][e & 1]);
-                l[n][0] += p[0] + p[2];
-                l[n][1] += p[1] + p[3];
+                for (int n = 0; n < NT; ++n) {
+                    float p[4];
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    float t[4] = {p[0] * (sv[g][0] * vmul[g]), p[1] * (sv[g][0] * vmul[g]),
-                                  p[2] * (sv[g][1] * vmul[g]), p[3] * (sv[g][1] * vmul[g])};
-                    if (full) {
-                        ab[g][n][0] = fmaf(p[0], bv[g][0], fmaf(p[2], bv[g][1], ab[g][n][0]));
-                        ab[g][n][1] = fmaf(p[1], bv[g][0], fmaf(p[3], bv[g][1], ab[g][n][1]));
-                    } else {                      // a token that this row does not see may be infinite or NaN
+                    for (int e = 0; e < 4; ++e) p[e] = ex2(fmaf(s[pc][n][e], cs[n][e & 1], nm[n][e & 1]));
+                    l[n][0] += p[0] + p[2];
+                    l[n][1] += p[1] + p[3];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (s[n][e] == -INFINITY) t[e] = 0.0f;
-                            else ab[g][n][e & 1] = fmaf(p[e], bv[g][e >> 1], ab[g][n][e & 1]);
+                    for (int g = 0; g < KG; ++g) {
+                        const float m0 = sv[pc][g][0] * vmul[g], m1 = sv[pc][g][1] * vmul[g];
+                        float t[4] = {p[0] * m0, p[1] * m0, p[2] * m1, p[3] * m1};
+                        if (full) {
+                            ab[g][n][0] = fmaf(p[0], bv[pc][g][0], fmaf(p[2], bv[pc][g][1], ab[g][n][0]));
+                            ab[g][n][1] = fmaf(p[1], bv[pc][g][0], fmaf(p[3], bv[pc][g][1], ab[g][n][1]));
+                        } else {                  // a token that this row does not see may be infinite or NaN
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (s[pc][n][e] == -INFINITY) t[e] = 0.0f;
+                                else ab[g][n][e & 1] = fmaf(p[e], bv[pc][g][e >> 1], ab[g][n][e & 1]);
+                            }
                         }
+                        const __half2 x = __floats2half2_rn(t[0], t[1]);
+                        const __half2 y = __floats2half2_rn(t[2], t[3]);
+                        pb[g][n][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
+                        pb[g][n][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
                     }
-                    const __half2 x = __floats2half2_rn(t[0], t[1]);
-                    const __half2 y = __floats2half2_rn(t[2], t[3]);
-                    pb[g][n][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
-                    pb[g][n][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
                 }
-            }
-            // ---- O^T += V^T (p s)^T ----
+                // ---- O^T += V^T (p s)^T ----
+                const uint8_t* vp = kt + pc * Gm::PIECE + Gm::CODES + v_lane;
 #pragma unroll
-            for (int sb = 0; sb < SUBS; ++sb) {
-                const int g = sb * KS / G;
-                const int word = KS == 64 ? sb * 8 + r : sb * 4 + (r >> 1);
-                uint32_t w[4];
+                for (int sb = 0; sb < SUBS; ++sb) {
+                    const int g = sb * KS / G;
+                    uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {     // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-                    const int pos = (k >> 1) * 8 + (k & 1) * 4 + c;
-                    w[k] = *reinterpret_cast<const uint32_t*>(vt + pos * Gm::ROWB + (((word >> 2) ^ Gm::swz(pos)) << 4) + (word & 3) * 4);
-                }
-                if constexpr (KS == 64) {
-                    uint32_t xl = __byte_perm(w[0], w[1], 0x5410), xh = __byte_perm(w[0], w[1], 0x7632);
-                    uint32_t yl = __byte_perm(w[2], w[3], 0x5410), yh = __byte_perm(w[2], w[3], 0x7632);
+                    for (int k = 0; k < 4; ++k)   // tokens 2c, 2c + 1, 2c + 8, 2c + 9
+                        w[k] = *reinterpret_cast<const uint32_t*>(vp + sb * (KS / 32) * Gm::CP + k * 64);
+                    if constexpr (KS == 64) {
+                        uint32_t xl = __byte_perm(w[0], w[1], 0x5410), xh = __byte_perm(w[0], w[1], 0x7632);
+                        uint32_t yl = __byte_perm(w[2], w[3], 0x5410), yh = __byte_perm(w[2], w[3], 0x7632);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) { // nibbles 2j, 2j + 1 (rows r) and 2j + 4, 2j + 5 (rows r + 8)
-                        const uint32_t a0 = code_lo(xl), a1 = code_lo(xh), a2 = code_lo(yl), a3 = code_lo(yh);
-                        const uint32_t c0 = code_hi(xl), c1 = code_hi(xh), c2 = code_hi(yl), c3 = code_hi(yh);
+                        for (int j = 0; j < 2; ++j) {   // nibbles 2j, 2j + 1 (rows r) and 2j + 4, 2j + 5 (rows r + 8)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16(acc[sb * 4 + 2 * j][n], a0, a1, a2, a3, pb[g][n][0], pb[g][n][1]);
-                            mma_f16(acc[sb * 4 + 2 * j + 1][n], c0, c1, c2, c3, pb[g][n][0], pb[g][n][1]);
+                            for (int n = 0; n < NT; ++n) {
+                                mma_f16(acc[sb * 4 + 2 * j][n], nib_lo(xl), nib_lo(xh), nib_lo(yl), nib_lo(yh), pb[g][n][0], pb[g][n][1]);
+                                mma_f16(acc[sb * 4 + 2 * j + 1][n], nib_hi(xl), nib_hi(xh), nib_hi(yl), nib_hi(yh), pb[g][n][0], pb[g][n][1]);
+                            }
+                            xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8;
                         }
-                        xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8;
-                    }
-                } else {
-                    const uint32_t sel = (r & 1) ? 0x7632 : 0x5410;
-                    uint32_t x = __byte_perm(w[0], w[1], sel), y = __byte_perm(w[2], w[3], sel);
+                    } else {
+                        const uint32_t sel = (r & 1) ? 0x7632 : 0x5410;
+                        uint32_t x = __byte_perm(w[0], w[1], sel), y = __byte_perm(w[2], w[3], sel);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) { // nibble 2j (rows r) and 2j + 1 (rows r + 8) of this lane's half word
-                        const uint32_t a0 = code_lo(x), a1 = code_hi(x), a2 = code_lo(y), a3 = code_hi(y);
+                        for (int j = 0; j < 2; ++j) {   // nibble 2j (rows r) and 2j + 1 (rows r + 8) of this lane's half word
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(acc[sb * 2 + j][n], a0, a1, a2, a3, pb[g][n][0], pb[g][n][1]);
-                        x >>= 8; y >>= 8;
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(acc[sb * 2 + j][n], nib_lo(x), nib_hi(x), nib_lo(y), nib_hi(y), pb[g][n][0], pb[g][n][1]);
+                            x >>= 8; y >>= 8;
+                        }
                     }
                 }
             }
             __syncwarp();   // every lane has read the slot before it is refilled
+            st = st + 1 == NST ? 0 : st + 1;
         }
+        if (missing) atomicOr(a.err, DEVERR_INDEX);
         cp_wait<0>();
         __syncthreads();    // the ring becomes the merge buffer
 
@@ -701,7 +794,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                 const int row = 8 * n + 2 * c + e;
                 if (r == 0) {
                     // nothing seen (a NaN sum is not nothing)
-                    mo[row * (D + 4) + D] = thr[n][e] == -INFINITY && l[n][e] == 0.0f ? -INFINITY : mu[n][e];
+                    mo[row * (D + 4) + D] = thr[n][e] == -INFINITY && l[n][e] == 0.0f ? -INFINITY : -nm[n][e];
                     mo[row * (D + 4) + D + 1] = l[n][e];
                 }
 #pragma unroll
@@ -711,7 +804,9 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int dim = KS == 64 ? (mt >> 2) * 64 + 8 * r + (mt & 3) + 4 * h : (mt >> 1) * 32 + 4 * r + 2 * (mt & 1) + h;
-                        mo[row * (D + 4) + dim] = fmaf(acc[mt][n][e + 2 * h], inv, ab[g][n][e]);
+                        // the codes' weight, by the nibble that they came from
+                        const float w = (KS == 64 ? mt & 1 : h) ? 0x1p20f : 0x1p24f;
+                        mo[row * (D + 4) + dim] = fmaf(acc[mt][n][e + 2 * h] * w, inv, ab[g][n][e]);
                     }
                 }
             }
@@ -719,10 +814,11 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 
         // ---- the warps' results together; a whole item is finished here, a part goes to the workspace ----
         const bool whole = u0 == 0 && u1 == sp.units;
-        const int64_t pslot = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+        const int64_t pslot = 2 * blockIdx.x + (first_seg ? 0 : 1);
         for (int x = threadIdx.x; x < ROWS * (D / 4); x += THREADS) {
             const int row = x / (D / 4), d4 = (x % (D / 4)) * 4;
             const int rr = row0 + row;
+            if (rr >= a.rows) break;      // rows in order: nothing behind it
             const float* base = reinterpret_cast<const float*>(smem) + row * (D + 4);
             float m = -INFINITY;
 #pragma unroll
@@ -741,7 +837,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                 }
             }
             if (whole) {
-                if (rr < a.rows) {
+                {
                     const int i = rr / a.rep;
                     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
                     uint16_t* op = a.out + seq * a.o_b + i * a.o_t + (head * a.rep + rr - i * a.rep) * (int64_t)a.o_h + d4;
@@ -761,6 +857,15 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
         __syncthreads();    // the merge buffer becomes the ring again, q is rewritten
         first_seg = false;
     }
+    // sequences without a visible token: their rows are zeros
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (L.of(b).units == 0) {
+            const int64_t n = (int64_t)a.Tq * a.Hq * D;
+            for (int64_t i = threadIdx.x; i < n; i += THREADS) {
+                const int64_t th = i / D, t = th / a.Hq;
+                a.out[b * a.o_b + t * a.o_t + (th - t * a.Hq) * a.o_h + (i - th * D)] = 0;
+            }
+        }
 }
 
 // Joins the partial results of an item whose units several CTAs shared: the last segment of the CTA
@@ -768,105 +873,110 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 // item x when there are fewer items than CTAs, else the item that starts in CTA x's stretch and
 // reaches past it, if there is one.
 template <int D, typename XT>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ AttnArgs a, int grid, int ROWS, int by_item) {
-    __shared__ int64_t sched[6];
+__global__ void __launch_bounds__(THREADS) combine_kernel(const __grid_constant__ AttnArgs a, int grid, int ROWS, int by_item, int unit) {
     __shared__ float red[WARPS][D + 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = blockIdx.y;
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
-    if (warp == 0) {
-        const int64_t W = total_units(a, lane);
-        const int64_t n = sharing(W, grid);
-        const int64_t items = (int64_t)a.Hkv * a.rtiles;
-        int64_t first = -1, last = -1, slot = 0, it = 0, before = 0, units = 0, j = blockIdx.x;
-        int seq = 0;
-        if (by_item) {
-            seq = (int)(blockIdx.x / items);
-            it = blockIdx.x - seq * items;
-            units = seq_span(a, seq).units;
-            for (int b = lane; b < seq; b += 32) before += seq_span(a, b).units * items;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-            if (units > 0) {          // the CTA whose stretch holds the item's first unit
-                const int64_t s0 = before + it * units;
-                j = s0 * n / W;
-                while (j > 0 && cut(W, n, j) > s0) --j;
-                while (cut(W, n, j + 1) <= s0) ++j;
-            }
-        } else if (j < n - 1) {       // the item of CTA j's last unit
-            const int64_t hi = cut(W, n, j + 1);
-            find_seq(a, lane, hi - 1, &seq, &before);
-            units = seq_span(a, seq).units;
-            it = (hi - 1 - before) / units;
-        }
-        if (units > 0) {
-            const int64_t lo = cut(W, n, j), hi = cut(W, n, j + 1);
-            const int64_t s0 = before + it * units, s1 = s0 + units;
-            if (s1 > hi && s0 >= lo) {
-                first = j;
-                slot = s0 > lo ? 1 : 0;               // not CTA j's first segment, unless the item starts its stretch
-                last = j + 1;
-                while (last + 1 < n && cut(W, n, last + 1) < s1) ++last;
-            }
-        }
-        if (lane == 0) {
-            sched[0] = first; sched[1] = last; sched[2] = slot; sched[3] = seq;
-            sched[4] = it / a.rtiles;
-            sched[5] = it % a.rtiles * ROWS + row;
+    // the lengths are complete: the attention kernel waited for them before this one started
+    Lengths L(a, lane, unit);
+    const Shares sh(L.total(), grid);
+    const int items = a.Hkv * a.rtiles;
+    int before = 0, j = blockIdx.x, first = -1, last = -1;
+    int seq = 0, it = 0, units = 0, slot0 = 0;
+    if (by_item) {
+        seq = blockIdx.x / items;
+        it = blockIdx.x - seq * items;
+        before = L.before(seq);
+        units = L.of(seq).units;
+        if (units > 0) j = sh.owner(before + it * units);   // the CTA whose stretch holds the item's first unit
+    } else if (j < sh.n - 1) {        // the item of CTA j's last unit
+        const int hi = sh.start(j + 1);
+        L.find(hi - 1, &seq, &before);
+        units = L.of(seq).units;
+        it = (hi - 1 - before) / units;
+    }
+    if (units > 0) {
+        const int lo = sh.start(j), hi = sh.start(j + 1);
+        const int s0 = before + it * units, s1 = s0 + units;
+        if (s1 > hi && s0 >= lo) {
+            first = j;
+            slot0 = s0 > lo ? 1 : 0;  // not CTA j's first segment, unless the item starts its stretch
+            last = sh.owner(s1 - 1);  // the CTA that holds its last unit
         }
     }
-    __syncthreads();
-    const int64_t first = sched[0], last = sched[1];
-    const int64_t rr = sched[5];
+    const int head = it / a.rtiles;
+    const int rr = (it - head * a.rtiles) * ROWS + row;
+    ptx::pdl_wait();                  // the partial results
+    ptx::pdl_launch_dependents();
     if (first < 0 || rr >= a.rows) return;
-    auto part = [&](int64_t k) { return (2 * (first + k) + (k == 0 ? sched[2] : 0)) * ROWS + row; };
-    const int np = (int)(last - first + 1);
-    float m = -INFINITY;
-    for (int k = lane; k < np; k += 32) m = fmaxf(m, __ldcg(a.part_ml + part(k) * 2));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    auto part = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0 ? slot0 : 0)) * ROWS + row; };
+    const int np = last - first + 1;
+    // a running reference per warp (parts k = warp, warp + 4, ...), four parts in flight
     constexpr int V = D / 32;
-    float o[V], ls = 0.0f;
+    float o[V], ls = 0.0f, m = -INFINITY;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int k = warp; k < np; k += WARPS) {
-        const int64_t p = part(k);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + p * 2));
-        float v[V];
+    for (int k0 = warp; k0 < np; k0 += 4 * WARPS) {
+        float2 ml[4];
+        float v[4][V];
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float2 u = __ldcg(reinterpret_cast<const float2*>(a.part_o + p * D + lane * V + e));
-            v[e] = u.x;
-            v[e + 1] = u.y;
-        }
-        if (ml.x != -INFINITY) {
-            const float f = ex2(ml.x - m);
-            ls = fmaf(f, ml.y, ls);
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * WARPS;
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            if (k < np) {
+                const int64_t p = part(k);
+                ml[u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + p * 2));
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf(f, v[e], o[e]);
+                for (int e = 0; e < V; e += 2) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(a.part_o + p * D + lane * V + e));
+                    v[u][e] = x.x;
+                    v[u][e + 1] = x.y;
+                }
+            }
         }
+        const float mn = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+        if (mn == -INFINITY) continue;                    // (a NaN reference is never -inf)
+        const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
+        ls *= f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (ml[u].x != -INFINITY) {
+                const float g = ex2(ml[u].x - mn);
+                ls = fmaf(g, ml[u].y, ls);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] = fmaf(g, v[u][e], o[e]);
+            }
+        m = mn;
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) red[warp][lane * V + e] = o[e];
-    if (lane == 0) red[warp][D] = ls;
+    if (lane == 0) {
+        red[warp][D] = ls;
+        red[warp][D + 1] = m;
+    }
     __syncthreads();
-    float lt = 0.0f;
+    float f[WARPS], lt = 0.0f, mt = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) lt += red[w][D];
+    for (int w = 0; w < WARPS; ++w) mt = fmaxf(mt, red[w][D + 1]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        f[w] = red[w][D + 1] == -INFINITY ? 0.0f : ex2(red[w][D + 1] - mt);
+        lt = fmaf(f[w], red[w][D], lt);
+    }
     const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-    const int i = (int)(rr / a.rep);
-    uint16_t* op = a.out + sched[3] * a.o_b + i * a.o_t + (sched[4] * a.rep + rr - (int64_t)i * a.rep) * a.o_h;
+    const int i = rr / a.rep;
+    uint16_t* op = a.out + seq * a.o_b + i * a.o_t + (head * a.rep + rr - i * a.rep) * (int64_t)a.o_h;
     for (int d = threadIdx.x; d < D; d += THREADS) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) t += red[w][d];
+        for (int w = 0; w < WARPS; ++w) t = fmaf(f[w], red[w][d], t);
         op[d] = float_to_half_bits(t * inv, XT{});
     }
 }
 
-template <int D, int G, int NT, typename XT>
+template <int D, int G, int NT, typename XT, bool FAST>
 cudaError_t launch_t(const AttnArgs& a, const AttnShape& s, cudaStream_t st) {
     using Gm = Geo<D, G, NT>;
     static std::mutex mu;
@@ -878,7 +988,7 @@ cudaError_t launch_t(const AttnArgs& a, const AttnShape& s, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
-            e = cudaFuncSetAttribute(attention_kernel<D, G, NT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
+            e = cudaFuncSetAttribute(attention_kernel<D, G, NT, XT, FAST>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
             if (e != cudaSuccess) return e;
             done[dev] = true;
         }
@@ -893,22 +1003,22 @@ cudaError_t launch_t(const AttnArgs& a, const AttnShape& s, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attention_kernel<D, G, NT, XT>, a);
+    e = cudaLaunchKernelEx(&cfg, attention_kernel<D, G, NT, XT, FAST>, a);
     if (e != cudaSuccess || !s.split) return e;
     const int64_t items = (int64_t)a.B * a.Hkv * a.rtiles;
     const int by_item = items <= s.grid ? 1 : 0;
     cfg.gridDim = dim3((unsigned)(by_item ? items : s.grid), (unsigned)(a.rows < Gm::ROWS ? a.rows : Gm::ROWS));
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, combine_kernel<D, XT>, a, s.grid, (int)Gm::ROWS, by_item);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<D, XT>, a, s.grid, (int)Gm::ROWS, by_item, unit_tokens(D, NT));
 }
 
 template <int D, int G, typename XT>
 cudaError_t launch_n(const AttnArgs& a, const AttnShape& s, cudaStream_t st) {
     switch (s.nt) {
-        case 1: return launch_t<D, G, 1, XT>(a, s, st);
-        case 2: return launch_t<D, G, 2, XT>(a, s, st);
+        case 1: return a.fast ? launch_t<D, G, 1, XT, true>(a, s, st) : launch_t<D, G, 1, XT, false>(a, s, st);
+        case 2: return a.fast ? launch_t<D, G, 2, XT, true>(a, s, st) : launch_t<D, G, 2, XT, false>(a, s, st);
         case 4:
-            if constexpr (D <= 128) return launch_t<D, G, 4, XT>(a, s, st);
+            if constexpr (D <= 128) return a.fast ? launch_t<D, G, 4, XT, true>(a, s, st) : launch_t<D, G, 4, XT, false>(a, s, st);
             break;
     }
     return cudaErrorInvalidValue;

@@ -53,11 +53,20 @@ struct AttnArgs {
     int window;                 // 0: none
     float scale_log2;           // softmax scale * log2(e)
     int fast;                   // 1: 16-token tiles lie inside a page and copy as whole 16-byte pieces
+    uint32_t k_page, k_slot, v_page, v_slot;   // fast: strides of the codes in bytes
+    int unit_slots;             // fast: a unit's tokens past whole pages
     int split;                  // 1: a combine launch follows (an item's units may be shared by CTAs)
     float* part_o;              // [2 * grid][8 * NT][D]
     float* part_ml;             // [2 * grid][8 * NT][2]
     int* err;
 };
+
+// How the kernel's tiles go by head size and n tiles: 16-token pieces of a warp's tile (two where the
+// registers of up to 8 query rows allow it), tokens of a work unit (a tile per warp, four warps), and
+// CTAs that fit an SM.
+constexpr int pieces_of(int D, int nt) { return nt == 1 && D <= 128 ? 2 : 1; }
+constexpr int unit_tokens(int D, int nt) { return 64 * pieces_of(D, nt); }
+constexpr int ctas_per_sm(int D, int nt) { return (D == 256 || nt == 4) ? 2 : 3; }
 
 // A launch's shape, by sizes only: NT (n tiles of 8 query rows), CTAs, workspace bytes.
 struct AttnShape {

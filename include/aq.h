@@ -333,8 +333,8 @@ aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots,
  *   to see; a query that sees nothing gives zeros.
  * pages: DEVICE pointer to int64 page ids, row b (at pages + b * pages_row) the pages of sequence
  *   b in order, max_pages of them; entries past a sequence's last page are not read.  A length
- *   outside [0, max_pages * S] is clamped, a page id outside [0, P) drops the tokens around it;
- *   both set the device error AQ_ERR_INDEX, and neither reads outside the cache.  Slots past a
+ *   outside [0, max_pages * S] is clamped, the tokens of a page id outside [0, P) count as
+ *   zeros; both set the device error AQ_ERR_INDEX, and neither reads outside the cache.  Slots past a
  *   sequence's end may hold anything, NaN scales included.
  * workspace: DEVICE memory of at least the bytes aq_kv_attention_workspace gives for the same q,
  *   k_wq and max_pages, 16-byte aligned, used by this call only while it runs on its stream.

@@ -22,7 +22,7 @@ def side(P=3, H=2, S=16, D=128, group=64, dtype=BF):
 
 
 def V(t):
-    return None if t is None else aq.view(t)
+    return None if t is None else ctypes.byref(aq.view(t))
 
 
 def no_device():
@@ -134,7 +134,7 @@ def test_append_accepts_interleaved_halves_up_to_the_launch(lib):
 
 # ---------------------------------------------------------------------------
 
-def attention(lib, q, kc, vc, out, group=64, bits=4, pages=True, lengths=True, max_pages=2, scale=1.0, window=0, ws="fit", row=2,
+def attention(lib, q, kc, vc, out, group=64, bits=4, pages=True, lengths=True, max_pages=64, scale=1.0, window=0, ws="fit", row=2,
               short=0):
     need = ctypes.c_size_t()
     ids = torch.zeros(8, dtype=torch.int64)

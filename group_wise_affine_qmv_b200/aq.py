@@ -100,7 +100,7 @@ def load_library(path: str = LIB_PATH):
         lib.aq_kv_attention.argtypes = [vp] * 7 + [ci, ci, vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_float, ci, vp, vp,
                                                   ctypes.c_size_t, vp]
         lib.aq_kv_attention.restype = ci
-        lib.aq_moe_swiglu_workspace.argtypes = [ctypes.c_int64, ci, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.aq_moe_swiglu_workspace.argtypes = [ctypes.c_int64, ci, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
         lib.aq_moe_swiglu_workspace.restype = ci
         lib.aq_moe_swiglu.argtypes = [vp, vp, ci, ci] + [vp] * 9 + [ci, ci, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
         lib.aq_moe_swiglu.restype = ci
@@ -400,7 +400,7 @@ def aq_moe_swiglu(x, logits, top_k: int, gate, up, down, group: int, bits: int, 
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
     with _On(x) as stream:
         need = ctypes.c_size_t()
-        _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, gate[0].shape[-2], ctypes.byref(need)))
+        _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, x.shape[1], gate[0].shape[-2], ctypes.byref(need)))
         ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
         vx, vl, *banks, vr, vy = _views(x, logits, *gate, *up, *down, residual, out)
         _check(lib, lib.aq_moe_swiglu(vx, vl, top_k, 1 if norm_topk else 0, *banks, group, bits, rms_eps, vr, vy,

@@ -605,11 +605,12 @@ aq_status check_bank(const aq_view* wq, const aq_view* sc, const aq_view* bi, co
     return AQ_OK;
 }
 
-aq_status check_moe_sizes(int64_t T, int top_k, int64_t N) {
+aq_status check_moe_sizes(int64_t T, int top_k, int64_t K, int64_t N) {
     if (T > aq::moe::MAX_TOKENS)
         return fail(AQ_ERR_UNSUPPORTED, "%lld tokens (up to %d; aq_qmm_t_grouped takes more)", (long long)T, aq::moe::MAX_TOKENS);
     if (top_k < 1 || top_k > aq::moe::MAX_TOPK) return fail(AQ_ERR_UNSUPPORTED, "top_k=%d (1..%d)", top_k, aq::moe::MAX_TOPK);
-    if (N < 0 || N > (1 << 20)) return fail(AQ_ERR_UNSUPPORTED, "experts of %lld rows (up to 2^20)", (long long)N);
+    if (K < 0 || K > (1 << 20) || N < 0 || N > (1 << 20))
+        return fail(AQ_ERR_UNSUPPORTED, "model size %lld, experts of %lld rows (up to 2^20)", (long long)K, (long long)N);
     return AQ_OK;
 }
 
@@ -1252,13 +1253,13 @@ AQ_API aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq
     return AQ_OK;
 }
 
-AQ_API aq_status aq_moe_swiglu_workspace(int64_t tokens, int top_k, int64_t n, size_t* bytes) {
+AQ_API aq_status aq_moe_swiglu_workspace(int64_t tokens, int top_k, int64_t k, int64_t n, size_t* bytes) {
     g_msg[0] = 0;
     if (!bytes) return fail(AQ_ERR_NULL, "bytes is NULL");
     if (tokens < 0) return fail(AQ_ERR_SHAPE, "tokens < 0");
-    aq_status st = check_moe_sizes(tokens, top_k, n);
+    aq_status st = check_moe_sizes(tokens, top_k, k, n);
     if (st != AQ_OK) return st;
-    *bytes = aq::moe::workspace_bytes(tokens, top_k, n);
+    *bytes = aq::moe::Layout(tokens, top_k, k, n).bytes;
     return AQ_OK;
 }
 
@@ -1285,10 +1286,9 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
     if (y->shape[0] != T || y->shape[1] != K) return fail(AQ_ERR_SHAPE, "y must have x's shape");
     if (!wq_gate || wq_gate->rank != 3) return check_view(wq_gate, "gate", 3, 3);
     const int64_t N = wq_gate->shape[1];
-    if ((st = check_moe_sizes(T, top_k, N)) != AQ_OK) return st;
+    if ((st = check_moe_sizes(T, top_k, K, N)) != AQ_OK) return st;
     if (E < 1 || E > aq::moe::MAX_EXPERTS) return fail(AQ_ERR_UNSUPPORTED, "%lld experts (1..%d)", (long long)E, aq::moe::MAX_EXPERTS);
     if (top_k > E) return fail(AQ_ERR_SHAPE, "top_k=%d of %lld experts", top_k, (long long)E);
-    if (K > (1 << 20)) return fail(AQ_ERR_UNSUPPORTED, "model size %lld (up to 2^20)", (long long)K);
     aq::moe::Args a;
     memset(&a, 0, sizeof a);
     if ((st = check_bank(wq_gate, s_gate, b_gate, "gate", x->dtype, E, N, K, group, bits, &a.gate)) != AQ_OK) return st;
@@ -1301,7 +1301,8 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
         if (r->shape[0] != T || r->shape[1] != K) return fail(AQ_ERR_SHAPE, "r must have y's shape");
         if (overlaps(r, y) && !same_view(r, y)) return fail(AQ_ERR_OVERLAP, "r overlaps y (other than being the same view)");
     }
-    const size_t need = aq::moe::workspace_bytes(T, top_k, N);
+    const aq::moe::Layout lay(T, top_k, K, N);
+    const size_t need = lay.bytes;
     aq_view ws;
     memset(&ws, 0, sizeof ws);
     ws.data = workspace;
@@ -1319,7 +1320,6 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
     if (overlaps(&ws, x) || overlaps(&ws, y) || (r && overlaps(&ws, r))) return fail(AQ_ERR_OVERLAP, "the workspace overlaps x, r or y");
     if (T == 0 || K == 0) return AQ_OK;
     if (N == 0) return fail(AQ_ERR_SHAPE, "experts without rows");
-    if (!aligned16(x->data) || (T > 1 && x->stride[0] % 8 != 0)) return fail(AQ_ERR_ALIGN, "rows of x must be 16-byte aligned");
     if (!workspace) return fail(AQ_ERR_NULL, "workspace is NULL");
     if (workspace_bytes < need) return fail(AQ_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if (!aligned16(workspace)) return fail(AQ_ERR_ALIGN, "workspace must be 16-byte aligned");
@@ -1336,9 +1336,15 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
     a.K = (int)K;
     a.N = (int)N;
     uint8_t* w = (uint8_t*)workspace;
-    a.h_hi = (uint16_t*)w;
-    a.h_lo = (uint16_t*)(w + aq::moe::h_bytes(T, top_k, N));
-    a.h_sum = (float*)(w + 2 * aq::moe::h_bytes(T, top_k, N));
+    a.entries = (int*)w;
+    a.pairs = (uint16_t*)(w + lay.pairs);
+    a.weight = (float*)(w + lay.weight);
+    a.xh = (uint16_t*)(w + lay.xh);
+    a.xsum = (float*)(w + lay.xsum);
+    a.xfac = (float*)(w + lay.xfac);
+    a.h = (uint16_t*)(w + lay.h);
+    a.hscale = (float*)(w + lay.hscale);
+    a.hsum = (float*)(w + lay.hsum);
     a.y = y->data;
     a.y_row = y->stride[0];
     a.ydt = y->dtype;

@@ -32,9 +32,17 @@ struct Args {
     int T, E, topk, norm;
     int K, N;                   // model size, expert size
     Bank gate, up, down;
-    uint16_t* h_hi;             // workspace: [T * topk, N] bf16, the activations' leading 8 bits
-    uint16_t* h_lo;             //   ... and the next 8
-    float* h_sum;               // workspace: [T * topk, N / 16], sums of 16 activations
+    // workspace (Layout), written by the routing kernel ...
+    int* entries;               // [1 + MAX_ENTRIES]: how many, then expert | tokens << 16 of each
+    uint16_t* pairs;            // [MAX_ENTRIES][TB]: token * topk + choice of an entry's tokens
+    float* weight;              // [T * topk]
+    uint16_t* xh;               // [T, K] f16: x scaled by a power of two per token, permuted like the codes
+    float* xsum;                // [T, K / unit]: sums of xh over folds, in the codes' weight
+    float* xfac;                // [T]: what takes the sums back (and the RMS norm)
+    // ... and by the gate/up kernel
+    uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted
+    float* hscale;              // [T * topk, N / 16]: those powers of two
+    float* hsum;                // [T * topk, N / 16]: sums of 16 activations
     void* y;
     int64_t y_row;
     int ydt;                    // DT of y
@@ -44,9 +52,27 @@ struct Args {
     int cs;                     // CTAs of a cluster that share the experts of a block of y columns
 };
 
-// workspace bytes; every part starts on a 16-byte boundary
-inline size_t h_bytes(int64_t T, int64_t topk, int64_t N) { return ((size_t)T * topk * N * 2 + 15) / 16 * 16; }
-inline size_t workspace_bytes(int64_t T, int64_t topk, int64_t N) { return 2 * h_bytes(T, topk, N) + (size_t)T * topk * (N / 16) * 4; }
+constexpr int TB = 16;          // tokens of an entry
+constexpr int MAX_ENTRIES = MAX_TOKENS * MAX_TOPK;
+
+// Offsets of the workspace's parts, each on a 16-byte boundary, and its size.  (Sums of x are kept per
+// 32 codes or more: K / 32 of them at most.)
+struct Layout {
+    size_t pairs, weight, xh, xsum, xfac, h, hscale, hsum, bytes;
+    Layout(int64_t T, int64_t topk, int64_t K, int64_t N) {
+        auto up = [](size_t v) { return (v + 15) / 16 * 16; };
+        const size_t p = (size_t)T * topk;
+        pairs = up((1 + MAX_ENTRIES) * sizeof(int));
+        weight = pairs + up(p * TB * 2);
+        xh = weight + up(p * 4);
+        xsum = xh + up((size_t)T * K * 2);
+        xfac = xsum + up((size_t)T * (K / 32) * 4);
+        h = xfac + up((size_t)T * 4);
+        hscale = h + up(p * N * 2);
+        hsum = hscale + up(p * (N / 16) * 4);
+        bytes = hsum + up(p * (N / 16) * 4);
+    }
+};
 
 // instantiated in kernels_moe_b<BITS>_<type>.cu
 template <int BITS, bool BF>

@@ -1,28 +1,34 @@
-// moe_kernel.cuh -- a mixture-of-experts layer for a few tokens in two kernels.
+// moe_kernel.cuh -- a mixture-of-experts layer for a few tokens.
 //
 //     e_1 .. e_k = the top-k of logits[t], w = their softmax weights
-//     h[t, j]    = w_j silu(x[t] . Wg[e_j]^T) * (x[t] . Wu[e_j]^T)      (gate/up kernel)
-//     y[t]       = r[t] + sum_j h[t, j] . Wd[e_j]^T                     (down kernel)
+//     h[t, j]    = w_j silu(x[t] . Wg[e_j]^T) * (x[t] . Wu[e_j]^T)
+//     y[t]       = r[t] + sum_j h[t, j] . Wd[e_j]^T
 //
-// Every weight that some token chose is read once; at a few dozen tokens that traffic is all that
-// counts, so both kernels are built as streams of packed codes that never pause:
-//  - The routing costs no launch: every CTA of both kernels computes the top-k of all tokens itself
-//    (a few thousand logits from L2, a warp per token), and keeps per expert a 64-bit mask of its
-//    tokens.  An entry of the work list is an expert with up to 16 of its tokens.
-//  - A warp streams stages of 64 bytes x 32 weight rows through a ring in shared memory; the ring
-//    runs on across items, so the next item's codes are in flight while one is finished.  The
-//    warps of a CTA split K by stages (neighbouring warps read neighbouring 64 bytes).
-//  - The arithmetic is that of the warp-level dense kernel: codes expanded in registers into
-//    mma.sync A fragments (16 weight rows x 16 codes, 8 tokens per column tile), group sums of x
-//    from an all-ones tile, s D + b X folded in fp32.  Tokens of an expert are few, so a column
-//    tile is rarely full; it costs nothing, since the codes' expansion is what a stage takes.
-//  - The activations h keep 16 bits of mantissa between the kernels, as two bf16 (hi + lo), which
-//    the down kernel feeds as two MMAs: one 8-bit rounding there would cost as much accuracy as the
-//    rounding of y itself.  Their group sums come from the gate/up kernel's epilogue (sums of 16).
-//  - The down kernel computes its routing and stages its first weights while the gate/up kernel
-//    still runs (it waits only for h).  A CTA owns 32 columns of y for all tokens and walks the
-//    entries; a cluster of up to eight CTAs splits the entries and adds its tiles in rank order.
-//    No atomics: nothing depends on timing.
+// Three kernels, each a programmatic dependent of the one before: a small one for what depends on the
+// tokens alone (routing, and x in the form the next kernel multiplies), gate/up, and down.  Every
+// weight that some token chose is read once per 16 of its tokens; at a few dozen tokens that traffic is
+// what counts, so the two large kernels are streams of packed codes that never pause, and what is left
+// to care about is instructions per code:
+//  - Codes go to the tensor cores (mma.sync.m16n8k16, 16 weight rows x 16 codes, 8 tokens) as f16
+//    subnormals: a byte of a half, masked to one code, is already the f16 number code * 2^-24 (times 4 or
+//    16 where the code sits higher in the byte).  A pair of 8-bit codes takes one PRMT, a pair of 4-bit
+//    codes one AND and half a shift; the exact products and fp32 sums differ from those of the codes by
+//    powers of two only.  x is scaled by a power of two per token into f16's range (exact for bf16 and
+//    f16), its elements permuted and scaled to meet their codes' positions.
+//  - Sums of x per group come with it from the first kernel, so a group costs s D + b X, two FMAs per
+//    row and token.
+//  - A warp streams stages of 64 bytes x 32 weight rows through its own ring in shared memory with
+//    16-byte asynchronous copies; the ring runs on across items, so the next item's codes are in flight
+//    while one is finished.  Experts, token lists and scales are fetched ahead of their use.
+//  - gate/up: an item is 16 gate rows and the same 16 up rows of one expert, for up to 16 tokens.  A warp
+//    does an item alone, all of K, and ends with both sums of an activation in one lane.  Where there
+//    are too few items to fill the device the four warps of a CTA share one, a quarter of the stages each.
+//  - The activations pass on as f16 with a power of two per 16 of them (11 bits of mantissa: y is rounded
+//    to 8 or 11), so the down kernel multiplies subnormal codes again.
+//  - down: a CTA owns 32 columns of y for all tokens and walks the entries, its warps splitting N by
+//    stages; a cluster of up to eight CTAs splits the entries and adds its tiles in rank order.  It stages
+//    its first weights while the gate/up kernel still runs.  No atomics on results: nothing depends on
+//    timing.
 #pragma once
 
 #include <mutex>
@@ -35,8 +41,7 @@ namespace moe {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-constexpr int TB = 16;                 // tokens of an entry: two n8 tiles
-constexpr int NST = 5;                 // stages of a warp's ring
+constexpr int NST = 6;                 // stages of a warp's ring
 constexpr int ROWS = 32;               // weight rows of a stage
 constexpr int STAGE = ROWS * 64;       // bytes
 constexpr int RP = ROWS + 1;           // floats per token of a partial tile
@@ -44,7 +49,7 @@ constexpr int RP = ROWS + 1;           // floats per token of a partial tile
 template <int BITS, int G>
 struct Geo {
     static constexpr int SC = 512 / BITS;                 // codes of a row per stage (64 bytes)
-    static constexpr int KS = G < 64 ? G : 64;            // codes per sub-block (warp_mma_kernel.cuh)
+    static constexpr int KS = G < 64 ? G : 64;            // codes per sub-block: a lane holds KS / 4 in a row
     static constexpr int SUBS = SC / KS;
     static constexpr int STEPS = KS / 16;
     static constexpr int LB = KS * BITS / 32;             // bytes of a row per lane and sub-block
@@ -54,15 +59,58 @@ struct Geo {
     static_assert(LB >= 4, "a lane's codes fill whole words");
 };
 
-// ---- routing ----
+// Where element j of 16 consecutive ones goes in the order of the expanded codes, and the power of two
+// that its code carries: 8 bits in order; 4 bits (0,4) (1,5) (2,6) (3,7) of a word, odd ones 16 times;
+// 2 bits (j, j + 8) of a word, 4^(j % 4) times.
+template <int BITS>
+__device__ __forceinline__ int code_pos(int j) {
+    if constexpr (BITS == 8) return j;
+    else if constexpr (BITS == 4) return (j & 8) | ((j & 3) << 1) | ((j >> 2) & 1);
+    else return ((j & 7) << 1) | (j >> 3);
+}
+template <int BITS>
+__device__ __forceinline__ float code_scale(int j) {
+    if constexpr (BITS == 8) return 1.0f;
+    else if constexpr (BITS == 4) return (j & 1) ? 0.0625f : 1.0f;
+    else return __uint_as_float((127u - 2u * (uint32_t)(j & 3)) << 23);
+}
+// a lane's codes of one row and sub-block as pairs for the k steps
+template <int BITS, int STEPS>
+__device__ __forceinline__ void expand(const uint32_t* w, uint32_t (*a)[2]) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        if constexpr (BITS == 8) {
+            a[s][0] = __byte_perm(w[s], 0, 0x4140);
+            a[s][1] = __byte_perm(w[s], 0, 0x4342);
+        } else if constexpr (BITS == 4) {
+            const uint32_t v = (s & 1) ? w[s >> 1] >> 8 : w[s >> 1];
+            a[s][0] = v & 0x000F000Fu;
+            a[s][1] = v & 0x00F000F0u;
+        } else {
+            const uint32_t v = (s & 2) ? w[s >> 2] >> 8 : w[s >> 2];
+            a[s][0] = v & ((s & 1) ? 0x00300030u : 0x00030003u);
+            a[s][1] = v & ((s & 1) ? 0x00C000C0u : 0x000C000Cu);
+        }
+    }
+}
+constexpr float CODE = 0x1p24f;        // a code's weight in the sums
+
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// ---- routing and x ----
 
 struct Routing {
     uint64_t mask[MAX_EXPERTS];              // tokens of each expert
-    float weight[MAX_TOKENS * MAX_TOPK];     // per (token, choice)
     uint16_t sel[MAX_TOKENS * MAX_TOPK];     // the chosen expert, 0xffff: none
-    uint16_t entry[MAX_TOKENS * MAX_TOPK];   // work list: expert | token block << 12
+    uint16_t entry[MAX_ENTRIES];             // work list: expert | token block << 12
     int entries;
 };
+constexpr int PREP_WARPS = 16;
 
 __device__ __forceinline__ uint32_t ordered(float v) {   // order-preserving; NaN above everything, -inf is 0: never chosen
     if (v != v) return 0xffffffffu;
@@ -74,7 +122,7 @@ __device__ __forceinline__ uint32_t ordered(float v) {   // order-preserving; Na
 
 template <int EPL>
 __device__ __forceinline__ void route_tokens(const Args& a, Routing& R, int warp, int lane) {
-    for (int t = warp; t < a.T; t += WARPS) {
+    for (int t = warp; t < a.T; t += PREP_WARPS) {
         float v[EPL];
         uint32_t key[EPL];
 #pragma unroll
@@ -129,14 +177,65 @@ __device__ __forceinline__ void route_tokens(const Args& a, Routing& R, int warp
         sum = warp_sum(sum);
         if (lane < a.topk) {
             R.sel[t * a.topk + lane] = (uint16_t)chosen;
-            R.weight[t * a.topk + lane] = p / sum;
+            a.weight[t * a.topk + lane] = p / sum;
         }
     }
 }
 
-// Top-k, weights, masks and the work list, by the whole CTA.
-__device__ __forceinline__ void route(const Args& a, Routing& R, int warp, int lane) {
-    for (int e = threadIdx.x; e < a.E; e += THREADS) R.mask[e] = 0;
+// Block 0 routes all tokens; block 1 + t prepares token t.
+template <int BITS, typename XT, int G>
+__global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_constant__ Args a) {
+    using Gm = Geo<BITS, G>;
+    __shared__ Routing R;
+    __shared__ float red[2][PREP_WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::pdl_wait();                 // x and the logits may come from the kernel before, and the workspace be in use
+    ptx::pdl_launch_dependents();
+    if (blockIdx.x > 0) {
+        const int t = blockIdx.x - 1;
+        const uint16_t* x = a.x + t * a.x_row;
+        float am = 0.0f, s2 = 0.0f;
+        for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+            const float v = half_bits_to_float(__ldcg(x + k), XT{});
+            am = fmaxf(am, fabsf(v));
+            s2 = fmaf(v, v, s2);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        s2 = warp_sum(s2);
+        if (lane == 0) {
+            red[0][warp] = am;
+            red[1][warp] = s2;
+        }
+        __syncthreads();
+        am = s2 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < PREP_WARPS; ++w) {
+            am = fmaxf(am, red[0][w]);
+            s2 += red[1][w];
+        }
+        // 2^(14 - exponent of the largest value): exact products (an infinity's exponent stays in range)
+        const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255) - 127, -100), 127);
+        const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+        for (int u = warp; u < a.K / Gm::FU; u += PREP_WARPS) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < Gm::FU / 32; ++i) {
+                const int k = u * Gm::FU + lane + 32 * i, j = k & 15;
+                const float v = half_bits_to_float(__ldcg(x + k), XT{}) * up;
+                sum += v;
+                a.xh[(int64_t)t * a.K + (k & ~15) + code_pos<BITS>(j)] = float_to_half_bits(v * code_scale<BITS>(j), f16_t{});
+            }
+            sum = warp_sum(sum);
+            if (lane == 0) a.xsum[(int64_t)t * (a.K / Gm::FU) + u] = sum * (1.0f / CODE);
+        }
+        if (threadIdx.x == 0) {
+            const float norm = a.rms_eps > 0.0f ? rsqrtf(s2 / (float)a.K + a.rms_eps) : 1.0f;
+            a.xfac[t] = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * norm;
+        }
+        return;
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) R.mask[e] = 0;
     __syncthreads();
     if (a.E <= 128) route_tokens<4>(a, R, warp, lane);
     else route_tokens<MAX_EXPERTS / 32>(a, R, warp, lane);
@@ -158,119 +257,145 @@ __device__ __forceinline__ void route(const Args& a, Routing& R, int warp, int l
         if (lane == 0) R.entries = n;
     }
     __syncthreads();
-}
-
-// The tokens of an entry in a warp's own list: pair[i] = token * topk + choice.  Returns how many.
-__device__ __forceinline__ int entry_pairs(const Args& a, const Routing& R, int entry, uint16_t* pair, int lane) {
-    const int e = entry & 0xfff, first = (entry >> 12) * TB;
-    const uint64_t m = R.mask[e];
-    __syncwarp();
+    if (threadIdx.x == 0) a.entries[0] = R.entries;
+    for (int i = warp; i < R.entries; i += PREP_WARPS) {
+        const int e = R.entry[i] & 0xfff, first = (R.entry[i] >> 12) * TB;
+        const uint64_t m = R.mask[e];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int t = lane + 32 * half;
-        if ((m >> t) & 1) {
-            const int rank = __popcll(m & ((1ull << t) - 1)) - first;
-            if (rank >= 0 && rank < TB) {
-                int j = 0;
-                while (j + 1 < a.topk && R.sel[t * a.topk + j] != e) ++j;
-                pair[rank] = (uint16_t)(t * a.topk + j);
+        for (int half = 0; half < 2; ++half) {
+            const int t = lane + 32 * half;
+            if ((m >> t) & 1) {
+                const int rank = __popcll(m & ((1ull << t) - 1)) - first;
+                if (rank >= 0 && rank < TB) {
+                    int j = 0;
+                    while (j + 1 < a.topk && R.sel[t * a.topk + j] != e) ++j;
+                    a.pairs[i * TB + rank] = (uint16_t)(t * a.topk + j);
+                }
             }
         }
+        if (lane == 0) a.entries[1 + i] = e | (min(__popcll(m) - first, TB) << 16);
     }
-    __syncwarp();
-    const int n = __popcll(m) - first;
-    return n < TB ? n : TB;
 }
 
 // ---- streams of packed codes ----
 
-__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool live) {   // zeros where not live
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, int size) {   // size 0: zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 1) << 1; }   // spreads 32-byte reads over the banks
 
-// one lane's codes of sub-block sb of a stage's row
-template <int LB>
-__device__ __forceinline__ void lane_words(const uint8_t* stage, int row, int sb, int c, uint32_t* w) {
-    const int off = sb * 4 * LB + c * LB;
-    wm::load_lane_words<LB>(stage + row * 64 + (((off >> 4) ^ swz(row)) << 4) + (off & 15), w);
-}
-
-// A stage's scales or biases of one row: GPS halves from element `off`.
+// A stage's scales or biases of one row: GPS halves from p + g0.
 template <int GPS>
-__device__ __forceinline__ void load_sb(const uint16_t* p, int g0, int kg, bool vec, uint16_t (&v)[GPS]) {
+__device__ __forceinline__ void load_sb(const uint16_t* p, int g0, int kg, bool vec, uint32_t (&v)[(GPS + 1) / 2]) {
     if constexpr (GPS == 4) {
         if (vec) {
             const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + g0));
-            v[0] = (uint16_t)u.x; v[1] = (uint16_t)(u.x >> 16); v[2] = (uint16_t)u.y; v[3] = (uint16_t)(u.y >> 16);
+            v[0] = u.x; v[1] = u.y;
             return;
         }
     }
     if constexpr (GPS == 2) {
         if (vec) {
-            const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p + g0));
-            v[0] = (uint16_t)u; v[1] = (uint16_t)(u >> 16);
+            v[0] = __ldg(reinterpret_cast<const uint32_t*>(p + g0));
             return;
         }
     }
 #pragma unroll
-    for (int i = 0; i < GPS; ++i) v[i] = __ldg(p + min(g0 + i, kg - 1));
+    for (int i = 0; i < GPS; i += 2) {
+        v[i / 2] = __ldg(p + min(g0 + i, kg - 1));
+        if (i + 1 < GPS) v[i / 2] |= (uint32_t)__ldg(p + min(g0 + i + 1, kg - 1)) << 16;
+    }
 }
+template <typename XT>
+__device__ __forceinline__ float sb_value(const uint32_t* v, int i) {
+    const uint32_t w = v[i >> 1];
+    return half_bits_to_float((uint16_t)((i & 1) ? w >> 16 : w), XT{});
+}
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, int i0, int n, bool vec, float (&v)[N]) {
+    if constexpr (N == 4) {
+        if (vec) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(p + i0));
+            v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+            return;
+        }
+    }
+    if constexpr (N == 2) {
+        if (vec) {
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(p + i0));
+            v[0] = u.x; v[1] = u.y;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i0 + i < n ? __ldcg(p + i0 + i) : 0.0f;
+}
+
+// The power of two 2^(e - 14) with 2^e above v, in f16's range around v.
+__device__ __forceinline__ float scale_for(float v) {
+    const int ex = min(max((int)((__float_as_uint(v) >> 23) & 255) - 126, -100), 127);
+    return __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float v) { return __uint_as_float(0x7F000000u - __float_as_uint(v)); }
 
 // ---- gate/up ----
 
-template <int BITS, typename XT, int G>
+// SHARED: the CTA's warps share an item, each a quarter of its stages; else a warp has items of its own.
+template <int BITS, typename XT, int G, bool SHARED>
 __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
-    constexpr bool BF = std::is_same<XT, bf16_t>::value;
-    constexpr float OFF = (BF && BITS < 8) ? 128.0f : 0.0f;
-    constexpr int GPS = Gm::GPS;
+    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* rings = smem;
-    float* red = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);          // [2][WARPS][TB][RP]
-    float* sqs = red + 2 * WARPS * TB * RP;                                     // [2][WARPS][TB]
-    Routing& R = *reinterpret_cast<Routing*>(sqs + 2 * WARPS * TB);
-    __shared__ uint16_t pairs[WARPS][TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
+    uint8_t* ring = smem + warp * NST * STAGE;
+    const uint32_t ring_s = ptx::smem_u32(ring);
+    float* red = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);          // SHARED: [2][WARPS][TB][RP]
 
-    ptx::pdl_wait();                 // x and the logits may come from the kernel before
-    ptx::pdl_launch_dependents();    // after the wait: the down kernel reads the logits before its own
-    route(a, R, warp, lane);
+    ptx::pdl_wait();                 // routing and x
+    ptx::pdl_launch_dependents();    // after the wait: the down kernel reads the routing before its own
 
     const int nb_all = a.N / 16;
-    const int items = R.entries * nb_all;
-    const int kg = a.K / G;
+    const int items = __ldcg(a.entries) * nb_all;
+    const int kg = a.K / G, ku = a.K / Gm::FU;
     const int nst = (a.K + Gm::SC - 1) / Gm::SC;
-    const int nsw = (nst - warp + WARPS - 1) / WARPS;        // stages of this warp per item
+    const int s0 = SHARED ? warp : 0;
+    constexpr int SSTEP = SHARED ? WARPS : 1;
+    const int nsw = nst > s0 ? (nst - s0 + SSTEP - 1) / SSTEP : 0;   // stages of this warp per item
     const int row_bytes = a.K * BITS / 8;
-    uint8_t* ring = rings + warp * NST * STAGE;
-    const uint32_t ring_s = ptx::smem_u32(ring);
+    const int first = SHARED ? blockIdx.x : blockIdx.x * WARPS + warp;
+    const int step = SHARED ? gridDim.x : gridDim.x * WARPS;
+    const bool xvec = ku % GPS == 0;
 
-    // load cursor: item and stage of the next load
-    int l_item = blockIdx.x, l_s = 0, l_slot = 0;
+    // load cursor: the item, stage and ring slot of the next load, its rows' addresses, and the expert of
+    // the item after it
+    int l_item = first, l_s = 0, l_slot = 0, l_next = 0;
+    const uint8_t *l_gate = nullptr, *l_up = nullptr;
+    if (l_item < items) l_next = __ldcg(a.entries + 1 + l_item / nb_all);
     auto issue = [&]() {
         if (l_item < items && nsw > 0) {
-            const int ent = R.entry[l_item / nb_all], e = ent & 0xfff, n0 = (l_item % nb_all) * 16;
-            const int off = (warp + l_s * WARPS) * 64;
-            const uint8_t* gp = reinterpret_cast<const uint8_t*>(a.gate.wq + e * a.gate.w_exp);
-            const uint8_t* up = reinterpret_cast<const uint8_t*>(a.up.wq + e * a.up.w_exp);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (lane >> 2) + 8 * i, ch = lane & 3;
-                const int n = n0 + (row & 15);
-                const uint8_t* src = (row < 16 ? gp + n * a.gate.w_row * 4 : up + n * a.up.w_row * 4) + off + ch * 16;
-                const bool live = off + ch * 16 < row_bytes;
-                cp16z(ring_s + l_slot * STAGE + row * 64 + ((ch ^ swz(row)) << 4), live ? src : gp, live);
-            }
-            if (l_s == 0) {      // the scales and biases of the item's rows on their way to L2
+            if (l_s == 0) {
+                const int ent = l_item / nb_all, n0 = (l_item - ent * nb_all) * 16;
+                const int e = l_next & 0xffff;
+                if (l_item + step < items) l_next = __ldcg(a.entries + 1 + (l_item + step) / nb_all);
+                l_gate = reinterpret_cast<const uint8_t*>(a.gate.wq + e * a.gate.w_exp + (n0 + r) * a.gate.w_row) + c * 16;
+                l_up = reinterpret_cast<const uint8_t*>(a.up.wq + e * a.up.w_exp + (n0 + r) * a.up.w_row) + c * 16;
+                // the scales and biases of the item's rows on their way to L2
                 const int64_t so = (int64_t)(n0 + (lane & 15)) * kg;
                 ptx::prefetch_l2(lane < 16 ? a.gate.scales + e * a.gate.s_exp + so : a.up.scales + e * a.up.s_exp + so);
                 ptx::prefetch_l2(lane < 16 ? a.gate.biases + e * a.gate.b_exp + so : a.up.biases + e * a.up.b_exp + so);
             }
+            const int off = (s0 + l_s * SSTEP) * 64;
+            const int size = off + c * 16 < row_bytes ? 16 : 0;
+            const int o = size ? off : 0;
+            const uint32_t dst = ring_s + l_slot * STAGE + r * 64 + ((c ^ swz(r)) << 4);
+            cp16z(dst, l_gate + o, size);
+            cp16z(dst + 8 * 64, l_gate + o + 32 * a.gate.w_row, size);
+            cp16z(dst + 16 * 64, l_up + o, size);
+            cp16z(dst + 24 * 64, l_up + o + 32 * a.up.w_row, size);
             if (++l_s == nsw) {
                 l_s = 0;
-                l_item += gridDim.x;
+                l_item += step;
             }
             if (++l_slot == NST) l_slot = 0;
         }
@@ -279,161 +404,177 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) issue();
 
+    // the first item's entry and tokens (later ones are fetched an item ahead)
+    int next_ent = 0, next_pair = 0;
+    auto fetch_item = [&](int item) {
+        if (item < items) {
+            const int ent = item / nb_all;
+            next_ent = __ldcg(a.entries + 1 + ent);
+            next_pair = __ldcg(a.pairs + ent * TB + (lane & 15));
+        }
+    };
+    fetch_item(first);
+
     int slot = 0, buf = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
-        const int ent = R.entry[item / nb_all], e = ent & 0xfff, nb = item % nb_all, n0 = nb * 16;
-        const int nt = entry_pairs(a, R, ent, pairs[warp], lane);
-        const bool two = nt > 8;
-        // this lane's x rows (token r of each tile; past the last one: the last one)
+    for (int item = first; item < items; item += step, buf ^= 1) {
+        const int e = next_ent & 0xffff, nt = next_ent >> 16, pair = next_pair;
+        const int nb = item % nb_all, n0 = nb * 16;
+        fetch_item(item + step);
+        // this lane's x rows (token r of each tile; past the last one: the last one), and the sums of tokens 2c, 2c + 1
         const uint16_t* xr[2];
+        const float* xs[2][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int p = pairs[warp][min(8 * t + r, nt - 1)];
-            xr[t] = a.x + (p / a.topk) * a.x_row + c * (Gm::KS / 4);
+            const int tok = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1)) / a.topk;
+            xr[t] = a.xh + (int64_t)tok * a.K + c * (Gm::KS / 4);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                xs[t][q] = a.xsum + (int64_t)(__shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1)) / a.topk) * ku;
         }
         // rows r and r + 8 of gate (0, 1) and up (2, 3)
-        const uint16_t *sp[4], *bp[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Bank& B = i < 2 ? a.gate : a.up;
-            const int64_t ro = (int64_t)(n0 + r + 8 * (i & 1)) * kg;
-            sp[i] = B.scales + e * B.s_exp + ro;
-            bp[i] = B.biases + e * B.b_exp + ro;
-        }
-        float acc[2][2][4], sq[2][4];
+        const uint16_t *gs = a.gate.scales + e * a.gate.s_exp + (int64_t)(n0 + r) * kg, *gb = a.gate.biases + e * a.gate.b_exp + (int64_t)(n0 + r) * kg;
+        const uint16_t *us = a.up.scales + e * a.up.s_exp + (int64_t)(n0 + r) * kg, *ub = a.up.biases + e * a.up.b_exp + (int64_t)(n0 + r) * kg;
+        float acc[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sq[t][q] = 0.0f;
-        const uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
 
+        auto stages = [&](auto tiles) {
+            constexpr int NT = decltype(tiles)::value;
 #pragma unroll 1
-        for (int s = 0; s < nsw; ++s) {
-            const int st = warp + s * WARPS;
-            uint16_t sv[4][GPS], bv[4][GPS];
-            const int g0 = st * Gm::SC / G;
+            for (int s = 0; s < nsw; ++s) {
+                const int st = s0 + s * SSTEP;
+                uint32_t sv[4][(GPS + 1) / 2], bv[4][(GPS + 1) / 2];
+                const int g0 = st * Gm::SC / G;
+                const bool vec = a.gate.svec;
+                load_sb<GPS>(gs, g0, kg, vec, sv[0]);
+                load_sb<GPS>(gs + 8 * kg, g0, kg, vec, sv[1]);
+                load_sb<GPS>(us, g0, kg, vec, sv[2]);
+                load_sb<GPS>(us + 8 * kg, g0, kg, vec, sv[3]);
+                load_sb<GPS>(gb, g0, kg, vec, bv[0]);
+                load_sb<GPS>(gb + 8 * kg, g0, kg, vec, bv[1]);
+                load_sb<GPS>(ub, g0, kg, vec, bv[2]);
+                load_sb<GPS>(ub + 8 * kg, g0, kg, vec, bv[3]);
+                float X[NT][2][GPS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                load_sb<GPS>(sp[i], g0, kg, a.gate.svec, sv[i]);
-                load_sb<GPS>(bp[i], g0, kg, a.gate.svec, bv[i]);
-            }
-            constexpr int XV = Gm::KS / 32;          // 16-byte pieces of x per lane, tile and sub-block
-            uint4 xv[2][Gm::SUBS * XV];
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (t == 0 || two)
+                    for (int q = 0; q < 2; ++q) load_floats<GPS>(xs[t][q], st * GPS, ku, xvec, X[t][q]);
+                constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4;      // the whole stage's x in registers
+                uint4 xv[NT][AHEAD ? Gm::SUBS * XV : XV];
+                auto load_x = [&](int sb, int at) {
+                    const int k0 = st * Gm::SC + sb * Gm::KS;
 #pragma unroll
-                    for (int sb = 0; sb < Gm::SUBS; ++sb) {
-                        const int k0 = st * Gm::SC + sb * Gm::KS;
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int v = 0; v < XV; ++v)
-                            xv[t][sb * XV + v] = k0 < a.K ? __ldcg(reinterpret_cast<const uint4*>(xr[t] + k0) + v) : make_uint4(0, 0, 0, 0);
-                    }
-            issue();
-            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-            __syncwarp();
-            const uint8_t* stage = ring + slot * STAGE;
-            float d[2][2][4], xs[2][4];
+                            xv[t][at + v] = k0 < a.K ? __ldcg(reinterpret_cast<const uint4*>(xr[t] + k0) + v) : make_uint4(0, 0, 0, 0);
+                };
+                if constexpr (AHEAD)
 #pragma unroll
-            for (int sb = 0; sb < Gm::SUBS; ++sb) {
-                if (sb % Gm::SPF == 0)
+                    for (int sb = 0; sb < Gm::SUBS; ++sb) load_x(sb, sb * XV);
+                issue();
+                asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+                __syncwarp();
+                const uint8_t* stage = ring + slot * STAGE + r * 64;
+                float d[2][NT][4];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) d[0][t][q] = d[1][t][q] = xs[t][q] = 0.0f;
-                uint32_t fr[4][Gm::STEPS][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[Gm::LB / 4];
-                    lane_words<Gm::LB>(stage, r + 8 * i, sb, c, w);
-                    wm::expand_row<BITS, BF, Gm::STEPS>(w, fr[i]);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (t == 0 || two) {
-                        const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xv[t][sb * XV]);
-#pragma unroll
-                        for (int k = 0; k < Gm::STEPS; ++k) {
-#pragma unroll
-                            for (int m = 0; m < 2; ++m)
-                                wm::mma16816<BF>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
-                                                 xw[2 * k], xw[2 * k + 1]);
-                            wm::mma16816<BF>(xs[t], ONES, ONES, ONES, ONES, xw[2 * k], xw[2 * k + 1]);
-                            if (a.rms_eps > 0.0f)
-                                wm::mma16816<BF>(sq[t], xw[2 * k], xw[2 * k], xw[2 * k + 1], xw[2 * k + 1], xw[2 * k], xw[2 * k + 1]);
-                        }
-                    }
-                if (sb % Gm::SPF == Gm::SPF - 1) {
-                    const int f = sb / Gm::SPF;
+                for (int sb = 0; sb < Gm::SUBS; ++sb) {
+                    if constexpr (!AHEAD) load_x(sb, 0);
+                    uint32_t fr[4][Gm::STEPS][2];
+                    const int off = sb * 4 * Gm::LB + c * Gm::LB;
+                    const uint8_t* wp = stage + (((off >> 4) ^ swz(r)) << 4) + (off & 15);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int m = i >> 1, h = i & 1;
-                        const float ss = half_bits_to_float(sv[i][f], XT{});
-                        float bb = half_bits_to_float(bv[i][f], XT{});
-                        if (OFF != 0.0f) bb = fmaf(-OFF, ss, bb);
+                        uint32_t w[Gm::LB / 4];
+                        wm::load_lane_words<Gm::LB>(wp + i * 8 * 64, w);
+                        expand<BITS, Gm::STEPS>(w, fr[i]);
+                    }
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xv[t][AHEAD ? sb * XV : 0]);
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, xs[t][q], acc[m][t][2 * h + q]));
+                        for (int k = 0; k < Gm::STEPS; ++k)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                if (sb % Gm::SPF == 0 && k == 0)
+                                    mma0(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], xw[2 * k], xw[2 * k + 1]);
+                                else
+                                    wm::mma16816<false>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
+                                                        xw[2 * k], xw[2 * k + 1]);
+                            }
+                    }
+                    if (sb % Gm::SPF == Gm::SPF - 1) {
+                        const int f = sb / Gm::SPF;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = i >> 1, h = i & 1;
+                            const float ss = sb_value<XT>(sv[i], f), bb = sb_value<XT>(bv[i], f);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q)
+                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, X[t][q][f], acc[m][t][2 * h + q]));
+                        }
                     }
                 }
+                __syncwarp();
+                if (++slot == NST) slot = 0;
             }
-            __syncwarp();
-            if (++slot == NST) slot = 0;
-        }
-        // ---- the warps' slices of K together; silu(gate) * up * weight ----
-        float* rw = red + (buf * WARPS + warp) * TB * RP;
+        };
+        if (nt > 8) stages(std::integral_constant<int, 2>{});
+        else stages(std::integral_constant<int, 1>{});
+
+        // ---- silu(gate) * up * weight, for columns r and r + 8 and tokens 2c, 2c + 1 of each tile ----
+        if constexpr (SHARED) {      // the warps' slices of K together, in slice order, by the first warp's lanes
+            float* rw = red + buf * WARPS * 16 * 32;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) rw[(warp * 16 + m * 8 + t * 4 + q) * 32 + lane] = acc[m][t][q];
+            __syncthreads();
+            if (warp != 0) continue;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int w = 1; w < WARPS; ++w) acc[m][t][q] += rw[(w * 16 + m * 8 + t * 4 + q) * 32 + lane];
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t == 1 && nt <= 8) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int tok = 8 * t + 2 * c + q;
+                const int i = 8 * t + 2 * c + q;
+                const bool live = i < nt;
+                const int p = __shfl_sync(0xffffffffu, pair, live ? i : 0);
+                const float fac = __ldcg(a.xfac + p / a.topk), w = __ldcg(a.weight + p);
+                const float v0 = wm::silu(acc[0][t][q] * CODE * fac) * (acc[1][t][q] * CODE * fac) * w;
+                const float v1 = wm::silu(acc[0][t][2 + q] * CODE * fac) * (acc[1][t][2 + q] * CODE * fac) * w;
+                float m = fmaxf(fabsf(v0), fabsf(v1)), sum = v0 + v1;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) rw[tok * RP + 16 * m + 8 * h + r] = acc[m][t][2 * h + q];
-            }
-        if (c == (r >> 1))
-#pragma unroll
-            for (int t = 0; t < 2; ++t) sqs[(buf * WARPS + warp) * TB + 8 * t + r] = (r & 1) ? sq[t][1] : sq[t][0];
-        __syncthreads();
-        for (int i = threadIdx.x; i < TB * 16; i += THREADS) {
-            const int tok = i >> 4, col = i & 15;
-            float g = 0.0f, u = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float* q = red + (buf * WARPS + w) * TB * RP + tok * RP;
-                g += q[col];
-                u += q[16 + col];
-                s2 += sqs[(buf * WARPS + w) * TB + tok];
-            }
-            float hv = 0.0f;
-            const bool live = tok < nt;
-            const int p = pairs[warp][live ? tok : 0];
-            if (a.rms_eps > 0.0f) {
-                const float sc = rsqrtf(s2 / (float)a.K + a.rms_eps);
-                g *= sc;
-                u *= sc;
-            }
-            const float v = wm::silu(g) * u * R.weight[p];
-            const uint16_t hi = float_to_half_bits(v, bf16_t{});
-            const float hf = half_bits_to_float(hi, bf16_t{});
-            // an infinite activation has no remainder
-            const uint16_t lo = isfinite(v) && isfinite(hf) ? float_to_half_bits(v - hf, bf16_t{}) : 0;
-            hv = hf + half_bits_to_float(lo, bf16_t{});
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) hv += __shfl_xor_sync(0xffffffffu, hv, o);
-            if (live) {
-                a.h_hi[(int64_t)p * a.N + n0 + col] = hi;
-                a.h_lo[(int64_t)p * a.N + n0 + col] = lo;
-                if (col == 0) a.h_sum[(int64_t)p * nb_all + nb] = hv;
+                for (int o = 4; o < 32; o <<= 1) {
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
+                const float sc = scale_for(m), inv = pow2_inverse(sc);
+                if (live) {
+                    uint16_t* hp = a.h + (int64_t)p * a.N + n0;
+                    hp[code_pos<BITS>(r)] = float_to_half_bits(v0 * inv * code_scale<BITS>(r), f16_t{});
+                    hp[code_pos<BITS>(r + 8)] = float_to_half_bits(v1 * inv * code_scale<BITS>(r + 8), f16_t{});
+                    if (r == 0) {
+                        a.hscale[(int64_t)p * nb_all + nb] = sc;
+                        a.hsum[(int64_t)p * nb_all + nb] = sum;
+                    }
+                }
             }
         }
     }
@@ -445,46 +586,44 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 template <int BITS, typename XT, int G>
 __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
-    constexpr float OFF = BITS < 8 ? 128.0f : 0.0f;      // h is bf16 whatever x's type
-    constexpr int GPS = Gm::GPS;
+    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     float* yt = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);           // [WARPS][T][RP]
-    Routing& R = *reinterpret_cast<Routing*>(yt + ((WARPS * a.T * RP + 3) & ~3));
-    __shared__ uint16_t pairs[WARPS][TB];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
     const int cs = a.cs;
     const int rank = cs > 1 ? (int)ptx::cluster_ctarank() : 0;
     const int row0 = (int)(blockIdx.x / cs) * ROWS;      // first column of y
 
-    route(a, R, warp, lane);     // the logits are complete: the gate/up kernel waited for them before this one started
-    for (int i = threadIdx.x; i < WARPS * a.T * RP; i += THREADS) yt[i] = 0.0f;
-
-    const int kg = a.N / G;
+    const int entries = __ldcg(a.entries);               // complete: the gate/up kernel waited for it before this one started
+    const int kg = a.N / G, nb_all = a.N / 16;
     const int nst = (a.N + Gm::SC - 1) / Gm::SC;
-    const int nsw = (nst - warp + WARPS - 1) / WARPS;
+    const int nsw = nst > warp ? (nst - warp + WARPS - 1) / WARPS : 0;
     const int row_bytes = a.N * BITS / 8;
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_s = ptx::smem_u32(ring);
 
-    int l_ent = rank, l_s = 0, l_slot = 0;
+    int l_ent = rank, l_s = 0, l_slot = 0, l_next = 0;
+    const uint8_t* l_row[4] = {nullptr, nullptr, nullptr, nullptr};
+    if (l_ent < entries) l_next = __ldcg(a.entries + 1 + l_ent);
     auto issue = [&]() {
-        if (l_ent < R.entries && nsw > 0) {
-            const int e = R.entry[l_ent] & 0xfff;
-            const int off = (warp + l_s * WARPS) * 64;
-            const uint8_t* wp = reinterpret_cast<const uint8_t*>(a.down.wq + e * a.down.w_exp);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (lane >> 2) + 8 * i, ch = lane & 3;
-                const int n = min(row0 + row, a.K - 1);
-                const bool live = off + ch * 16 < row_bytes;
-                cp16z(ring_s + l_slot * STAGE + row * 64 + ((ch ^ swz(row)) << 4), live ? wp + n * a.down.w_row * 4 + off + ch * 16 : wp, live);
-            }
+        if (l_ent < entries && nsw > 0) {
             if (l_s == 0) {
+                const int e = l_next & 0xffff;
+                if (l_ent + cs < entries) l_next = __ldcg(a.entries + 1 + l_ent + cs);
+                const uint8_t* wp = reinterpret_cast<const uint8_t*>(a.down.wq + e * a.down.w_exp) + c * 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l_row[i] = wp + min(row0 + r + 8 * i, a.K - 1) * a.down.w_row * 4;
                 const int64_t so = (int64_t)min(row0 + lane, a.K - 1) * kg;
                 ptx::prefetch_l2(a.down.scales + e * a.down.s_exp + so);
                 ptx::prefetch_l2(a.down.biases + e * a.down.b_exp + so);
             }
+            const int off = (warp + l_s * WARPS) * 64;
+            const int size = off + c * 16 < row_bytes ? 16 : 0;
+            const int o = size ? off : 0;
+            const uint32_t dst = ring_s + l_slot * STAGE + r * 64 + ((c ^ swz(r)) << 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp16z(dst + i * 8 * 64, l_row[i] + o, size);
             if (++l_s == nsw) {
                 l_s = 0;
                 l_ent += cs;
@@ -495,34 +634,36 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
     };
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) issue();
+    for (int i = threadIdx.x; i < WARPS * a.T * RP; i += THREADS) yt[i] = 0.0f;
+    int next_ent = 0, next_pair = 0;
+    auto fetch_entry = [&](int ent) {
+        if (ent < entries) {
+            next_ent = __ldcg(a.entries + 1 + ent);
+            next_pair = __ldcg(a.pairs + ent * TB + (lane & 15));
+        }
+    };
+    fetch_entry(rank);
     __syncthreads();             // the y tiles are zero
 
-    ptx::pdl_wait();             // h
+    ptx::pdl_wait();             // the activations
     ptx::pdl_launch_dependents();
 
     int slot = 0;
     float* yw = yt + warp * a.T * RP;
-    for (int ent = rank; ent < R.entries; ent += cs) {
-        const int en = R.entry[ent], e = en & 0xfff;
-        const int nt = entry_pairs(a, R, en, pairs[warp], lane);
-        const bool two = nt > 8;
-        const uint16_t *hr[2], *lr[2];
-        const float* xsum[2][2];                         // sums of tokens 2c and 2c + 1 of each tile
+    for (int ent = rank; ent < entries; ent += cs) {
+        const int e = next_ent & 0xffff, nt = next_ent >> 16, pair = next_pair;
+        fetch_entry(ent + cs);
+        int po[2], px[2][2];     // rows of the workspace: token r of each tile; tokens 2c and 2c + 1
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int64_t o = (int64_t)pairs[warp][min(8 * t + r, nt - 1)] * a.N + c * (Gm::KS / 4);
-            hr[t] = a.h_hi + o;
-            lr[t] = a.h_lo + o;
+            po[t] = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1));
 #pragma unroll
-            for (int q = 0; q < 2; ++q) xsum[t][q] = a.h_sum + (int64_t)pairs[warp][min(8 * t + 2 * c + q, nt - 1)] * (a.N / 16);
+            for (int q = 0; q < 2; ++q) px[t][q] = __shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1));
         }
-        const uint16_t *sp[4], *bp[4];
+        const uint16_t *sp = a.down.scales + e * a.down.s_exp, *bp = a.down.biases + e * a.down.b_exp;
+        int ro[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t ro = (int64_t)min(row0 + r + 8 * i, a.K - 1) * kg;
-            sp[i] = a.down.scales + e * a.down.s_exp + ro;
-            bp[i] = a.down.biases + e * a.down.b_exp + ro;
-        }
+        for (int i = 0; i < 4; ++i) ro[i] = min(row0 + r + 8 * i, a.K - 1) * kg;
         float acc[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -531,105 +672,135 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.0f;
 
+        auto stages = [&](auto tiles) {
+            constexpr int NT = decltype(tiles)::value;
 #pragma unroll 1
-        for (int s = 0; s < nsw; ++s) {
-            const int st = warp + s * WARPS;
-            uint16_t sv[4][GPS], bv[4][GPS];
-            const int g0 = st * Gm::SC / G;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                load_sb<GPS>(sp[i], g0, kg, a.down.svec, sv[i]);
-                load_sb<GPS>(bp[i], g0, kg, a.down.svec, bv[i]);
-            }
-            issue();
-            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-            __syncwarp();
-            const uint8_t* stage = ring + slot * STAGE;
-            float d[2][2][4];
-#pragma unroll
-            for (int sb = 0; sb < Gm::SUBS; ++sb) {
-                const int k0 = st * Gm::SC + sb * Gm::KS;
-                if (k0 >= a.N) break;
-                if (sb % Gm::SPF == 0)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) d[0][t][q] = d[1][t][q] = 0.0f;
-                uint32_t fr[4][Gm::STEPS][2];
+            for (int s = 0; s < nsw; ++s) {
+                const int st = warp + s * WARPS;
+                uint32_t sv[4][(GPS + 1) / 2], bv[4][(GPS + 1) / 2];
+                const int g0 = st * Gm::SC / G;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t w[Gm::LB / 4];
-                    lane_words<Gm::LB>(stage, r + 8 * i, sb, c, w);
-                    wm::expand_row<BITS, true, Gm::STEPS>(w, fr[i]);
+                    load_sb<GPS>(sp + ro[i], g0, kg, a.down.svec, sv[i]);
+                    load_sb<GPS>(bp + ro[i], g0, kg, a.down.svec, bv[i]);
                 }
-                constexpr int XV = Gm::KS / 32;
+                constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4;      // the whole stage's activations in registers
+                uint4 hv[NT][AHEAD ? Gm::SUBS * XV : XV];
+                float hs[NT][AHEAD ? Gm::SUBS : 1];                  // their power of two (this lane's 16)
+                auto load_h = [&](int sb, int at) {
+                    const int k0 = st * Gm::SC + sb * Gm::KS;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (t == 0 || two) {
-                        uint4 hv[XV], lv[XV];
+                    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                        for (int v = 0; v < XV; ++v) {
-                            hv[v] = __ldcg(reinterpret_cast<const uint4*>(hr[t] + k0) + v);
-                            lv[v] = __ldcg(reinterpret_cast<const uint4*>(lr[t] + k0) + v);
+                        for (int v = 0; v < XV; ++v)
+                            hv[t][at * XV + v] = k0 < a.N ? __ldcg(reinterpret_cast<const uint4*>(a.h + (int64_t)po[t] * a.N + k0 + c * (Gm::KS / 4)) + v)
+                                                          : make_uint4(0, 0, 0, 0);
+                        hs[t][at] = k0 < a.N ? __ldcg(a.hscale + (int64_t)po[t] * nb_all + (k0 + c * (Gm::KS / 4)) / 16) : 0x1p-114f;
+                    }
+                };
+                if constexpr (AHEAD)
+#pragma unroll
+                    for (int sb = 0; sb < Gm::SUBS; ++sb) load_h(sb, sb);
+                issue();
+                asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+                __syncwarp();
+                const uint8_t* stage = ring + slot * STAGE + r * 64;
+                float df[2][NT][4];                      // a fold's sum, in true units
+#pragma unroll
+                for (int sb = 0; sb < Gm::SUBS; ++sb) {
+                    if constexpr (!AHEAD) load_h(sb, 0);
+                    uint32_t fr[4][Gm::STEPS][2];
+                    const int off = sb * 4 * Gm::LB + c * Gm::LB;
+                    const uint8_t* wp = stage + (((off >> 4) ^ swz(r)) << 4) + (off & 15);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[Gm::LB / 4];
+                        wm::load_lane_words<Gm::LB>(wp + i * 8 * 64, w);
+                        expand<BITS, Gm::STEPS>(w, fr[i]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        // the sub-block's activations on the largest of its powers of two
+                        const float own = hs[t][AHEAD ? sb : 0];
+                        float top = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 2));
+                        if constexpr (Gm::KS == 64) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        const __half2 f = __float2half2_rn(own * pow2_inverse(top));
+                        uint32_t* hw = reinterpret_cast<uint32_t*>(&hv[t][AHEAD ? sb * XV : 0]);
+#pragma unroll
+                        for (int k = 0; k < 4 * XV; ++k) {
+                            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hw[k]), f);
+                            hw[k] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        const uint32_t *hw = reinterpret_cast<const uint32_t*>(hv), *lw = reinterpret_cast<const uint32_t*>(lv);
+                        float d[2][4];
 #pragma unroll
                         for (int k = 0; k < Gm::STEPS; ++k)
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                wm::mma16816<true>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
-                                                   hw[2 * k], hw[2 * k + 1]);
-                                wm::mma16816<true>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
-                                                   lw[2 * k], lw[2 * k + 1]);
+                                if (k == 0)
+                                    mma0(d[m], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k], hw[2 * k + 1]);
+                                else
+                                    wm::mma16816<false>(d[m], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k],
+                                                        hw[2 * k + 1]);
+                            }
+                        // tokens 2c and 2c + 1 on their own power of two
+                        const float m0 = __shfl_sync(0xffffffffu, top, 8 * c) * CODE, m1 = __shfl_sync(0xffffffffu, top, 8 * c + 4) * CODE;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (sb % Gm::SPF == 0) {
+                                    df[m][t][2 * h] = d[m][2 * h] * m0;
+                                    df[m][t][2 * h + 1] = d[m][2 * h + 1] * m1;
+                                } else {
+                                    df[m][t][2 * h] = fmaf(d[m][2 * h], m0, df[m][t][2 * h]);
+                                    df[m][t][2 * h + 1] = fmaf(d[m][2 * h + 1], m1, df[m][t][2 * h + 1]);
+                                }
                             }
                     }
-                if (sb % Gm::SPF == Gm::SPF - 1) {
-                    const int f = sb / Gm::SPF;
-                    const int x0 = (st * Gm::SC + f * Gm::FU) / 16;
-                    float X[2][2];
+                    if (sb % Gm::SPF == Gm::SPF - 1) {
+                        const int f = sb / Gm::SPF;
+                        const int x0 = (st * Gm::SC + f * Gm::FU) / 16;
+                        float X[NT][2];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            X[t][q] = 0.0f;
-                            if (t == 0 || two)
+                            for (int q = 0; q < 2; ++q) {
+                                X[t][q] = 0.0f;
+                                const float* xp = a.hsum + (int64_t)px[t][q] * nb_all + x0;
+                                if (x0 < nb_all)
 #pragma unroll
-                                for (int i = 0; i < Gm::FU / 16; i += 2) {
-                                    X[t][q] += __ldcg(xsum[t][q] + x0 + i);
-                                    X[t][q] += __ldcg(xsum[t][q] + x0 + i + 1);
-                                }
+                                    for (int i = 0; i < Gm::FU / 16; ++i) X[t][q] += __ldcg(xp + i);
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = i >> 1, h = i & 1;
+                            const float ss = sb_value<XT>(sv[i], f), bb = sb_value<XT>(bv[i], f);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q)
+                                    acc[m][t][2 * h + q] = fmaf(ss, df[m][t][2 * h + q], fmaf(bb, X[t][q], acc[m][t][2 * h + q]));
                         }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int m = i >> 1, h = i & 1;
-                        const float ss = half_bits_to_float(sv[i][f], XT{});
-                        float bb = half_bits_to_float(bv[i][f], XT{});
-                        if (OFF != 0.0f) bb = fmaf(-OFF, ss, bb);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, X[t][q], acc[m][t][2 * h + q]));
                     }
                 }
+                __syncwarp();
+                if (++slot == NST) slot = 0;
             }
-            __syncwarp();
-            if (++slot == NST) slot = 0;
-        }
-        // this warp's slice of K into its own tile of y
+        };
+        if (nt > 8) stages(std::integral_constant<int, 2>{});
+        else stages(std::integral_constant<int, 1>{});
+        // this warp's slice of N into its own tile of y
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int i = 8 * t + 2 * c + q;
-                if (i < nt) {
-                    float* yp = yw + (pairs[warp][i] / a.topk) * RP;
+            for (int q = 0; q < 2; ++q)
+                if (8 * t + 2 * c + q < nt) {
+                    float* yp = yw + (px[t][q] / a.topk) * RP;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) yp[16 * m + 8 * h + r] += acc[m][t][2 * h + q];
                 }
-            }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
@@ -666,8 +837,8 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 template <int BITS, typename XT, int G>
 cudaError_t launch_t(const Args& a, cudaStream_t st) {
     const size_t ring = (size_t)WARPS * NST * STAGE;
-    const size_t smem1 = ring + (2 * WARPS * TB * RP + 2 * WARPS * TB) * sizeof(float) + sizeof(Routing);
-    const size_t smem2 = ring + ((WARPS * a.T * RP + 3) & ~3) * sizeof(float) + sizeof(Routing);
+    const size_t smem_shared = ring + 2 * WARPS * 16 * 32 * sizeof(float);
+    const size_t smem_down = ring + WARPS * a.T * RP * sizeof(float);
     constexpr int SMEM_MAX = 160 * 1024;
     static std::mutex mu;
     static bool done[64] = {false};
@@ -678,10 +849,12 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
-            e = cudaFuncSetAttribute(gate_up_kernel<BITS, XT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(down_kernel<BITS, XT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
-            if (e != cudaSuccess) return e;
+            const void* fns[3] = {(const void*)gate_up_kernel<BITS, XT, G, false>, (const void*)gate_up_kernel<BITS, XT, G, true>,
+                                  (const void*)down_kernel<BITS, XT, G>};
+            for (const void* f : fns) {
+                e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+                if (e != cudaSuccess) return e;
+            }
             done[dev] = true;
         }
     }
@@ -693,20 +866,32 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    // as many items as the tokens could choose, at most what fits the device at once
-    const int64_t pairs = (int64_t)a.T * a.topk;
-    const int64_t most = pairs < a.E + pairs / TB ? pairs : a.E + pairs / TB;
-    const int64_t items = most * (a.N / 16);
-    cfg.gridDim = dim3((unsigned)(items < 148 * 4 ? items : 148 * 4));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem1;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G>, a);
+    cfg.gridDim = dim3((unsigned)(1 + a.T));
+    cfg.blockDim = dim3(32 * PREP_WARPS);
+    e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT, G>, a);
+    if (e != cudaSuccess) return e;
+    // as many items as the tokens could choose, at most what fits the device at once (four CTAs an SM); with
+    // fewer items than half the device's warps, four warps to an item
+    const int64_t pairs = (int64_t)a.T * a.topk;
+    const int64_t most = pairs < a.E + pairs / TB ? pairs : a.E + pairs / TB;
+    const int64_t items = most * (a.N / 16), all = 148 * 4;
+    cfg.blockDim = dim3(THREADS);
+    if (items * 2 <= all * WARPS) {
+        cfg.gridDim = dim3((unsigned)(items < all ? items : all));
+        cfg.dynamicSmemBytes = smem_shared;
+        e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, true>, a);
+    } else {
+        const int64_t ctas = (items + WARPS - 1) / WARPS;
+        cfg.gridDim = dim3((unsigned)(ctas < all ? ctas : all));
+        cfg.dynamicSmemBytes = ring;
+        e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, false>, a);
+    }
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)((a.K + ROWS - 1) / ROWS * a.cs));
-    cfg.dynamicSmemBytes = smem2;
+    cfg.dynamicSmemBytes = smem_down;
     cfg.numAttrs = a.cs > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G>, a);
 }

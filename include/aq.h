@@ -350,13 +350,13 @@ aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq_view* 
 aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64_t max_pages, size_t* bytes);
 
 /*
- * aq_moe_swiglu -- a whole mixture-of-experts layer for up to 64 tokens, in two launches:
+ * aq_moe_swiglu -- a whole mixture-of-experts layer for up to 64 tokens, in three launches:
  *     e_1 .. e_k = the top_k largest logits[t]  (of equal ones the lower expert; -inf is never chosen)
  *     w_j        = softmax over the chosen (norm_topk != 0) or over all E logits (0), in fp32
  *     y[t]       = r[t] + sum_j w_j * dequant(W_down[e_j]) .
  *                  (silu(n x[t] . dequant(W_gate[e_j])^T) * (n x[t] . dequant(W_up[e_j])^T))
  *   with n = 1 / sqrt(mean_k x[t, k]^2 + rms_eps) when rms_eps > 0 (as in aq_qmm_t_swiglu), else 1.
- * x [T, K] AQ_BF16 or AQ_F16, T <= 64, rows 16-byte aligned (row stride free otherwise);
+ * x [T, K] AQ_BF16 or AQ_F16, T <= 64, row stride free;
  * logits [T, E] AQ_F32, AQ_BF16 or AQ_F16, E <= 512 (for instance aq_qmm_t of x with the router's
  * weights into AQ_F32); 1 <= top_k <= 16, top_k <= E.
  * gate, up: [E, N, K*bits/32] with scales/biases [E, N, K/group]; down: [E, K, N*bits/32] with
@@ -367,10 +367,10 @@ aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64
  * A token whose logits are all -inf gets y = r (0 without).  A NaN logit counts as the largest
  * and makes its token's y NaN.
  * Every expert that some token chose is read once per 16 of its tokens; both contractions are exact
- * in W with fp32 sums; the weighted activations pass between the launches with 16 bits of
- * mantissa.  The same call gives the same bits; the order of a token's sum over its experts may
+ * in W with fp32 sums; x enters exactly, and the weighted activations pass between the launches
+ * with 11 bits of mantissa (relative to the largest of 16).  The same call gives the same bits; the order of a token's sum over its experts may
  * depend on which experts the other tokens chose.
- * workspace: DEVICE memory of at least the bytes aq_moe_swiglu_workspace(T, top_k, N) gives,
+ * workspace: DEVICE memory of at least the bytes aq_moe_swiglu_workspace(T, top_k, K, N) gives,
  *   16-byte aligned, used by this call only while it runs on its stream.
  */
 aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_k, int norm_topk, const aq_view* wq_gate,
@@ -378,7 +378,7 @@ aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_k, int 
                         const aq_view* b_up, const aq_view* wq_down, const aq_view* s_down, const aq_view* b_down,
                         int group, int bits, float rms_eps, const aq_view* r, const aq_view* y, void* workspace,
                         size_t workspace_bytes, void* stream);
-aq_status aq_moe_swiglu_workspace(int64_t tokens, int top_k, int64_t n, size_t* bytes);
+aq_status aq_moe_swiglu_workspace(int64_t tokens, int top_k, int64_t k, int64_t n, size_t* bytes);
 
 /* ---------------------------------------------------------------------- */
 /* Introspection (host only, no GPU work).                                 */

@@ -252,7 +252,7 @@ def bank(E, N, K, group=64, bits=4, dtype=BF):
     ("bits", "AQ_ERR_BITS"), ("group", "AQ_ERR_GROUP"), ("kmod", "AQ_ERR_GROUP"), ("nmod", "AQ_ERR_GROUP"), ("xdtype", "AQ_ERR_DTYPE"),
     ("ldtype", "AQ_ERR_DTYPE"), ("ydtype", "AQ_ERR_DTYPE"), ("sdtype", "AQ_ERR_DTYPE"), ("lrows", "AQ_ERR_SHAPE"), ("yshape", "AQ_ERR_SHAPE"),
     ("upshape", "AQ_ERR_SHAPE"), ("downshape", "AQ_ERR_SHAPE"), ("sshape", "AQ_ERR_SHAPE"), ("srows", "AQ_ERR_UNSUPPORTED"),
-    ("walign", "AQ_ERR_ALIGN"), ("xalign", "AQ_ERR_ALIGN"), ("rshape", "AQ_ERR_SHAPE"), ("rdtype", "AQ_ERR_DTYPE"), ("ry", "AQ_ERR_OVERLAP"),
+    ("walign", "AQ_ERR_ALIGN"), ("xodd", None), ("rshape", "AQ_ERR_SHAPE"), ("rdtype", "AQ_ERR_DTYPE"), ("ry", "AQ_ERR_OVERLAP"),
     ("yx", "AQ_ERR_OVERLAP"), ("yself", "AQ_ERR_OVERLAP"), ("ylogits", "AQ_ERR_OVERLAP"), ("eps", "AQ_ERR_SHAPE"), ("epsnan", "AQ_ERR_SHAPE"),
     ("null", "AQ_ERR_NULL"), ("wsnull", "AQ_ERR_NULL"), ("wsshort", "AQ_ERR_SHAPE"), ("wsodd", "AQ_ERR_ALIGN"), ("wsx", "AQ_ERR_OVERLAP"),
     ("xrank", "AQ_ERR_RANK"), ("grank", "AQ_ERR_RANK"),
@@ -307,7 +307,7 @@ def test_moe_refusals(lib, case, status):
         down[1] = torch.zeros(E, K, 4, dtype=BF)[..., :3]
     elif case == "walign":
         gate[0] = odd(gate[0].shape, torch.int32)
-    elif case == "xalign":
+    elif case == "xodd":
         x = odd((T, K), BF)
     elif case == "rshape":
         r = torch.zeros(T, N, dtype=BF)
@@ -334,7 +334,7 @@ def test_moe_refusals(lib, case, status):
         wp = None
     elif case == "wsshort":
         n = ctypes.c_size_t()
-        assert lib.aq_moe_swiglu_workspace(T, top_k, N, ctypes.byref(n)) == 0
+        assert lib.aq_moe_swiglu_workspace(T, top_k, K, N, ctypes.byref(n)) == 0
         wb = n.value - 1
     elif case == "wsodd":
         wp += 8

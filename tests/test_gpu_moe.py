@@ -4,8 +4,9 @@ Tolerance.  y = r + sum_j w_j Wd (silu(g) u), all sums fp32.  Rounding y is half
 K products whose codes carry an offset of at most 128 (removed through the group sums): each is off by at most
 e1 = 2^-19 sum_k |n x_k| (|s| (128 + code) + |b|) (MMAs of 16 products, at most 8 a group, each within 2^-23 of the
 magnitudes summed, and the folds of K/G groups over four warps, 2^-24 each of at most 2^4 of them one after another).
-h = w silu(g) u is off by |w| (|u| 1.1 e1 + |silu(g)| e1) (|silu'| <= 1.1) and 2^-17 |h| for the two bf16 that carry it;
-__expf and the divisions are within 2^-20 of h.  The down product adds 2^-19 sum |h| (|s| (128 + code) + |b|) and weighs
+h = w silu(g) u is off by |w| (|u| 1.1 e1 + |silu(g)| e1) (|silu'| <= 1.1); it is carried as f16 with a power of two per 16
+values (per 64 when multiplied), off by half a step of 11 bits, 2^-11 |h|, or where it is a subnormal by 2^-25 / 2^13 = 2^-38
+of the largest of its row; __expf and the divisions are within 2^-18 of h.  The down product adds 2^-19 sum |h| (|s| (128 + code) + |b|) and weighs
 the errors of h with |Wd|.
 """
 import numpy as np
@@ -56,7 +57,7 @@ def reference(x, logits, top_k, banks, norm, rms_eps, r, ydt):
             eg, eu = (2.0 ** -19 * (m.mag[e] @ xt.abs()) for m in (gate, up))
             s = g * torch.sigmoid(g)
             h = we * s * u
-            eh = we * (u.abs() * 1.1 * eg + s.abs() * eu + eg * eu) + (2.0 ** -17 + 2.0 ** -18) * h.abs()
+            eh = we * (u.abs() * 1.1 * eg + s.abs() * eu + eg * eu) + (2.0 ** -11 + 2.0 ** -18) * h.abs() + 2.0 ** -38 * h.abs().max()
             y[t] += down.v[e] @ h
             err[t] += down.v[e].abs() @ eh + 2.0 ** -19 * (down.mag[e] @ (h.abs() + eh))
     u = torch.finfo(ydt).eps / 2

@@ -20,7 +20,8 @@ struct Bank {
     const uint16_t* biases;
     int64_t w_row, w_exp;       // words
     int64_t s_exp, b_exp;       // elements
-    int svec;                   // 1: a stage's scales (and biases) of a row are one aligned vector load
+    int svec;                   // 1: a stage's scales (and biases) of a row are one aligned copy
+    int blk;                    // 1: those of 16 rows together are a 16-byte aligned run
 };
 
 struct Args {
@@ -36,8 +37,8 @@ struct Args {
     int* entries;               // [1 + MAX_ENTRIES]: how many, then expert | tokens << 16 of each
     uint16_t* pairs;            // [MAX_ENTRIES][TB]: token * topk + choice of an entry's tokens
     float* weight;              // [T * topk]
-    uint16_t* xh;               // [T, K] f16: x scaled by a power of two per token, permuted like the codes
-    float* xsum;                // [T, K / unit]: sums of xh over folds, in the codes' weight
+    uint16_t* xh;               // [T, x_pitch(K)] f16: x scaled by a power of two per token, permuted like the codes
+    float* xsum;                // [T, x_pitch(K) / fold]: sums of xh over folds, in the codes' weight
     float* xfac;                // [T]: what takes the sums back (and the RMS norm)
     // ... and by the gate/up kernel
     uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted
@@ -50,13 +51,17 @@ struct Args {
     int64_t r_row;
     float rms_eps;              // > 0: x normalised per token
     int cs;                     // CTAs of a cluster that share the experts of a block of y columns
+    int* err;
 };
 
 constexpr int TB = 16;          // tokens of an entry
 constexpr int MAX_ENTRIES = MAX_TOKENS * MAX_TOPK;
 
+// columns of prepared x, in whole stages of any width (2-bit stages hold 256 codes)
+__host__ __device__ constexpr int x_pitch(int K) { return (K + 255) / 256 * 256; }
+
 // Offsets of the workspace's parts, each on a 16-byte boundary, and its size.  (Sums of x are kept per
-// 32 codes or more: K / 32 of them at most.)
+// 32 codes or more.)
 struct Layout {
     size_t pairs, weight, xh, xsum, xfac, h, hscale, hsum, bytes;
     Layout(int64_t T, int64_t topk, int64_t K, int64_t N) {
@@ -65,8 +70,8 @@ struct Layout {
         pairs = up((1 + MAX_ENTRIES) * sizeof(int));
         weight = pairs + up(p * TB * 2);
         xh = weight + up(p * 4);
-        xsum = xh + up((size_t)T * K * 2);
-        xfac = xsum + up((size_t)T * (K / 32) * 4);
+        xsum = xh + up((size_t)T * x_pitch((int)K) * 2);
+        xfac = xsum + up((size_t)T * (x_pitch((int)K) / 32) * 4);
         h = xfac + up((size_t)T * 4);
         hscale = h + up(p * N * 2);
         hsum = hscale + up(p * (N / 16) * 4);

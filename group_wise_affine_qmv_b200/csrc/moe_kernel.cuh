@@ -19,7 +19,11 @@
 //    row and token.
 //  - A warp streams stages of 64 bytes x 32 weight rows through its own ring in shared memory with
 //    16-byte asynchronous copies; the ring runs on across items, so the next item's codes are in flight
-//    while one is finished.  Experts, token lists and scales are fetched ahead of their use.
+//    while one is finished.  Experts and token lists are fetched an item ahead.
+//  - Scales and biases of an item's rows are one dense run each, which a bulk copy brings whole.  (Copied
+//    stage by stage, 4 bytes a row, each 32-byte sector crosses from L2 eight times, as much traffic as the
+//    codes: 128 experts of 8 bits, 8 tokens, 225 against 139 us without the arithmetic.)  Rows with too many
+//    groups for that, and items that four warps share, copy them stage by stage.
 //  - gate/up: an item is 16 gate rows and the same 16 up rows of one expert, for up to 16 tokens.  A warp
 //    does an item alone, all of K, and ends with both sums of an activation in one lane.  Where there
 //    are too few items to fill the device the four warps of a CTA share one, a quarter of the stages each.
@@ -41,10 +45,11 @@ namespace moe {
 
 constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
-constexpr int NST = 6;                 // stages of a warp's ring
 constexpr int ROWS = 32;               // weight rows of a stage
-constexpr int STAGE = ROWS * 64;       // bytes
 constexpr int RP = ROWS + 1;           // floats per token of a partial tile
+constexpr int UP_GROUPS = 64;          // most groups of a row whose scales a warp of the gate/up kernel holds whole
+constexpr int DOWN_GROUPS = 256;       // ... and a CTA of the down kernel, twice
+constexpr uint64_t WAIT_NS = 2000000000ull;   // budget of a bounded wait
 
 template <int BITS, int G>
 struct Geo {
@@ -56,6 +61,13 @@ struct Geo {
     static constexpr int FU = G < SC ? G : SC;            // codes per fold: a group, or a stage's part of it
     static constexpr int SPF = FU / KS;
     static constexpr int GPS = SC / FU;                   // folds per stage
+    // A stage in shared memory: codes, and where they come stage by stage the rows' scales and biases (the 4 or 8
+    // aligned bytes around its folds).
+    static constexpr int SBB = GPS == 4 ? 8 : 4;
+    static constexpr int CODES = ROWS * 64;
+    static constexpr int stage(bool blk) { return CODES + (blk ? 0 : 2 * ROWS * SBB); }
+    static constexpr int NST = 4;                         // stages of a warp's ring
+    static constexpr int ring(bool blk) { return WARPS * NST * stage(blk); }
     static_assert(LB >= 4, "a lane's codes fill whole words");
 };
 
@@ -110,7 +122,7 @@ struct Routing {
     uint16_t entry[MAX_ENTRIES];             // work list: expert | token block << 12
     int entries;
 };
-constexpr int PREP_WARPS = 16;
+constexpr int PREP_WARPS = 32;
 
 __device__ __forceinline__ uint32_t ordered(float v) {   // order-preserving; NaN above everything, -inf is 0: never chosen
     if (v != v) return 0xffffffffu;
@@ -217,17 +229,18 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_cons
         // 2^(14 - exponent of the largest value): exact products (an infinity's exponent stays in range)
         const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255) - 127, -100), 127);
         const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-        for (int u = warp; u < a.K / Gm::FU; u += PREP_WARPS) {
+        const int kp = x_pitch(a.K), ku = kp / Gm::FU;       // padded with zeros to whole stages
+        for (int u = warp; u < ku; u += PREP_WARPS) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < Gm::FU / 32; ++i) {
                 const int k = u * Gm::FU + lane + 32 * i, j = k & 15;
-                const float v = half_bits_to_float(__ldcg(x + k), XT{}) * up;
+                const float v = k < a.K ? half_bits_to_float(__ldcg(x + k), XT{}) * up : 0.0f;
                 sum += v;
-                a.xh[(int64_t)t * a.K + (k & ~15) + code_pos<BITS>(j)] = float_to_half_bits(v * code_scale<BITS>(j), f16_t{});
+                a.xh[(int64_t)t * kp + (k & ~15) + code_pos<BITS>(j)] = float_to_half_bits(v * code_scale<BITS>(j), f16_t{});
             }
             sum = warp_sum(sum);
-            if (lane == 0) a.xsum[(int64_t)t * (a.K / Gm::FU) + u] = sum * (1.0f / CODE);
+            if (lane == 0) a.xsum[(int64_t)t * ku + u] = sum * (1.0f / CODE);
         }
         if (threadIdx.x == 0) {
             const float norm = a.rms_eps > 0.0f ? rsqrtf(s2 / (float)a.K + a.rms_eps) : 1.0f;
@@ -280,55 +293,65 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_cons
 // ---- streams of packed codes ----
 
 __device__ __forceinline__ void cp16z(uint32_t dst, const void* src, int size) {   // size 0: zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 __device__ __forceinline__ int swz(int row) { return ((row >> 1) & 1) << 1; }   // spreads 32-byte reads over the banks
 
-// A stage's scales or biases of one row: GPS halves from p + g0.
-template <int GPS>
-__device__ __forceinline__ void load_sb(const uint16_t* p, int g0, int kg, bool vec, uint32_t (&v)[(GPS + 1) / 2]) {
-    if constexpr (GPS == 4) {
-        if (vec) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + g0));
-            v[0] = u.x; v[1] = u.y;
-            return;
-        }
-    }
-    if constexpr (GPS == 2) {
-        if (vec) {
-            v[0] = __ldg(reinterpret_cast<const uint32_t*>(p + g0));
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < GPS; i += 2) {
-        v[i / 2] = __ldg(p + min(g0 + i, kg - 1));
-        if (i + 1 < GPS) v[i / 2] |= (uint32_t)__ldg(p + min(g0 + i + 1, kg - 1)) << 16;
-    }
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, int bytes) {   // 4 or 8
+    if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-template <typename XT>
-__device__ __forceinline__ float sb_value(const uint32_t* v, int i) {
-    const uint32_t w = v[i >> 1];
-    return half_bits_to_float((uint16_t)((i & 1) ? w >> 16 : w), XT{});
+// One row's scales (or biases) of a stage into the ring: the GPS halves from p + g0.  Where rows keep them
+// aligned (vec), one asynchronous copy of the 4 or 8 bytes that hold them (a single one, GPS 1, with its even
+// or odd neighbour); else through registers.
+template <int GPS, int SBB>
+__device__ __forceinline__ void copy_sb(uint32_t dst, const uint16_t* p, int g0, int kg, bool vec) {
+    if (vec) {
+        cp_small(dst, p + (GPS == 1 ? g0 & ~1 : g0), SBB);
+        return;
+    }
+    uint32_t w[SBB / 4];
+#pragma unroll
+    for (int i = 0; i < SBB / 4; ++i) {
+        // GPS 1: the value in both halves
+        const uint32_t lo = __ldg(p + min(g0 + 2 * i, kg - 1)), hi = GPS == 1 ? lo : (uint32_t)__ldg(p + min(g0 + 2 * i + 1, kg - 1));
+        w[i] = lo | (hi << 16);
+    }
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[0]) : "memory");
+    if constexpr (SBB == 8) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4), "r"(w[1]) : "memory");
+}
+// value f of a row's scales in the ring; g0: the stage's first group
+template <int GPS, typename XT>
+__device__ __forceinline__ float sb_value(const uint32_t* v, int f, int g0) {
+    if constexpr (GPS == 1) return half_bits_to_float((uint16_t)((g0 & 1) ? v[0] >> 16 : v[0]), XT{});
+    const uint32_t w = v[f >> 1];
+    return half_bits_to_float((uint16_t)((f & 1) ? w >> 16 : w), XT{});
+}
+// One scale (or bias) pair wait, bounded: on expiry the error word says so, and the results are void.
+__device__ __forceinline__ void wait_block(uint64_t* bar, uint32_t parity, int* err) {
+    volatile int never = 0;
+    if (!ptx::mbar_wait(bar, parity, &never, WAIT_NS)) atomicOr(err, DEVERR_TIMEOUT);
+}
+template <int SBB>
+__device__ __forceinline__ void read_sb(const uint8_t* p, uint32_t* v) {
+    if constexpr (SBB == 8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        v[0] = u.x; v[1] = u.y;
+    } else {
+        v[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
 }
 template <int N>
-__device__ __forceinline__ void load_floats(const float* p, int i0, int n, bool vec, float (&v)[N]) {
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {   // aligned
     if constexpr (N == 4) {
-        if (vec) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(p + i0));
-            v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-            return;
-        }
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(p));
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else if constexpr (N == 2) {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(p));
+        v[0] = u.x; v[1] = u.y;
+    } else {
+        v[0] = __ldcg(p);
     }
-    if constexpr (N == 2) {
-        if (vec) {
-            const float2 u = __ldcg(reinterpret_cast<const float2*>(p + i0));
-            v[0] = u.x; v[1] = u.y;
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = i0 + i < n ? __ldcg(p + i0 + i) : 0.0f;
 }
 
 // The power of two 2^(e - 14) with 2^e above v, in f16's range around v.
@@ -345,19 +368,29 @@ template <int BITS, typename XT, int G, bool SHARED>
 __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
     constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
+    constexpr int NST = Gm::NST, STAGE = Gm::stage(!SHARED), SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t sb_bar[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
+    const int kg = a.K / G;
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_s = ptx::smem_u32(ring);
-    float* red = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);          // SHARED: [2][WARPS][TB][RP]
+    float* red = reinterpret_cast<float*>(smem + Gm::ring(false));   // SHARED: [2][WARPS][16][32]
+    // not SHARED: this warp's item's scales and biases, [gate s, up s, gate b, up b][16 rows][kg]
+    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(true)) + warp * 64 * kg;
+    if (!SHARED) {
+        if (lane == 0) ptx::mbar_init(&sb_bar[warp], 1);
+        ptx::fence_mbar_init();
+        __syncwarp();
+    }
 
     ptx::pdl_wait();                 // routing and x
     ptx::pdl_launch_dependents();    // after the wait: the down kernel reads the routing before its own
 
     const int nb_all = a.N / 16;
     const int items = __ldcg(a.entries) * nb_all;
-    const int kg = a.K / G, ku = a.K / Gm::FU;
+    const int kp = x_pitch(a.K), ku = kp / Gm::FU;
     const int nst = (a.K + Gm::SC - 1) / Gm::SC;
     const int s0 = SHARED ? warp : 0;
     constexpr int SSTEP = SHARED ? WARPS : 1;
@@ -365,12 +398,12 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
     const int row_bytes = a.K * BITS / 8;
     const int first = SHARED ? blockIdx.x : blockIdx.x * WARPS + warp;
     const int step = SHARED ? gridDim.x : gridDim.x * WARPS;
-    const bool xvec = ku % GPS == 0;
 
     // load cursor: the item, stage and ring slot of the next load, its rows' addresses, and the expert of
     // the item after it
     int l_item = first, l_s = 0, l_slot = 0, l_next = 0;
     const uint8_t *l_gate = nullptr, *l_up = nullptr;
+    const uint16_t *l_sc = nullptr, *l_bi = nullptr;     // of row `lane` of the stage: 16 gate rows, 16 up rows
     if (l_item < items) l_next = __ldcg(a.entries + 1 + l_item / nb_all);
     auto issue = [&]() {
         if (l_item < items && nsw > 0) {
@@ -380,19 +413,28 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                 if (l_item + step < items) l_next = __ldcg(a.entries + 1 + (l_item + step) / nb_all);
                 l_gate = reinterpret_cast<const uint8_t*>(a.gate.wq + e * a.gate.w_exp + (n0 + r) * a.gate.w_row) + c * 16;
                 l_up = reinterpret_cast<const uint8_t*>(a.up.wq + e * a.up.w_exp + (n0 + r) * a.up.w_row) + c * 16;
-                // the scales and biases of the item's rows on their way to L2
-                const int64_t so = (int64_t)(n0 + (lane & 15)) * kg;
-                ptx::prefetch_l2(lane < 16 ? a.gate.scales + e * a.gate.s_exp + so : a.up.scales + e * a.up.s_exp + so);
-                ptx::prefetch_l2(lane < 16 ? a.gate.biases + e * a.gate.b_exp + so : a.up.biases + e * a.up.b_exp + so);
+                if constexpr (SHARED) {
+                    const Bank& B = lane < 16 ? a.gate : a.up;
+                    const int64_t so = (int64_t)(n0 + (lane & 15)) * kg;
+                    l_sc = B.scales + e * B.s_exp + so;
+                    l_bi = B.biases + e * B.b_exp + so;
+                } else if (lane < 4) {   // on their way to L2, for the bulk copies at the item's turn
+                    const Bank& B = (lane & 1) ? a.up : a.gate;
+                    ptx::prefetch_l2_bulk((lane < 2 ? B.scales + e * B.s_exp : B.biases + e * B.b_exp) + (int64_t)n0 * kg, 32 * kg);
+                }
             }
-            const int off = (s0 + l_s * SSTEP) * 64;
+            const int st = s0 + l_s * SSTEP, off = st * 64;
             const int size = off + c * 16 < row_bytes ? 16 : 0;
             const int o = size ? off : 0;
-            const uint32_t dst = ring_s + l_slot * STAGE + r * 64 + ((c ^ swz(r)) << 4);
+            const uint32_t slot0 = ring_s + l_slot * STAGE, dst = slot0 + r * 64 + ((c ^ swz(r)) << 4);
             cp16z(dst, l_gate + o, size);
             cp16z(dst + 8 * 64, l_gate + o + 32 * a.gate.w_row, size);
             cp16z(dst + 16 * 64, l_up + o, size);
             cp16z(dst + 24 * 64, l_up + o + 32 * a.up.w_row, size);
+            if constexpr (SHARED) {
+                copy_sb<GPS, SBB>(slot0 + Gm::CODES + lane * SBB, l_sc, st * Gm::SC / G, kg, a.gate.svec);
+                copy_sb<GPS, SBB>(slot0 + Gm::CODES + (ROWS + lane) * SBB, l_bi, st * Gm::SC / G, kg, a.gate.svec);
+            }
             if (++l_s == nsw) {
                 l_s = 0;
                 l_item += step;
@@ -414,10 +456,26 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
         }
     };
     fetch_item(first);
+    // one item's scales and biases, whole, into the block (four lanes, one run each)
+    auto load_block = [&](int item) {
+        if constexpr (!SHARED) {
+            if (item < items && lane < 4) {
+                const int e = next_ent & 0xffff, n0 = item % nb_all * 16;
+                const Bank& B = (lane & 1) ? a.up : a.gate;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sb_bar[warp], 128 * kg);
+                __syncwarp(0xf);
+                ptx::bulk_load(blk + lane * 16 * kg, (lane < 2 ? B.scales + e * B.s_exp : B.biases + e * B.b_exp) + (int64_t)n0 * kg,
+                               32 * kg, &sb_bar[warp]);
+            }
+            __syncwarp();
+        }
+    };
+    load_block(first);
 
+    uint32_t turn = 0;
     int slot = 0, buf = 0;
     for (int item = first; item < items; item += step, buf ^= 1) {
-        const int e = next_ent & 0xffff, nt = next_ent >> 16, pair = next_pair;
+        const int nt = next_ent >> 16, pair = next_pair;
         const int nb = item % nb_all, n0 = nb * 16;
         fetch_item(item + step);
         // this lane's x rows (token r of each tile; past the last one: the last one), and the sums of tokens 2c, 2c + 1
@@ -426,14 +484,11 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int tok = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1)) / a.topk;
-            xr[t] = a.xh + (int64_t)tok * a.K + c * (Gm::KS / 4);
+            xr[t] = a.xh + (int64_t)tok * kp + c * (Gm::KS / 4);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 xs[t][q] = a.xsum + (int64_t)(__shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1)) / a.topk) * ku;
         }
-        // rows r and r + 8 of gate (0, 1) and up (2, 3)
-        const uint16_t *gs = a.gate.scales + e * a.gate.s_exp + (int64_t)(n0 + r) * kg, *gb = a.gate.biases + e * a.gate.b_exp + (int64_t)(n0 + r) * kg;
-        const uint16_t *us = a.up.scales + e * a.up.s_exp + (int64_t)(n0 + r) * kg, *ub = a.up.biases + e * a.up.b_exp + (int64_t)(n0 + r) * kg;
         float acc[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -444,46 +499,64 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 
         auto stages = [&](auto tiles) {
             constexpr int NT = decltype(tiles)::value;
-#pragma unroll 1
-            for (int s = 0; s < nsw; ++s) {
-                const int st = s0 + s * SSTEP;
-                uint32_t sv[4][(GPS + 1) / 2], bv[4][(GPS + 1) / 2];
-                const int g0 = st * Gm::SC / G;
-                const bool vec = a.gate.svec;
-                load_sb<GPS>(gs, g0, kg, vec, sv[0]);
-                load_sb<GPS>(gs + 8 * kg, g0, kg, vec, sv[1]);
-                load_sb<GPS>(us, g0, kg, vec, sv[2]);
-                load_sb<GPS>(us + 8 * kg, g0, kg, vec, sv[3]);
-                load_sb<GPS>(gb, g0, kg, vec, bv[0]);
-                load_sb<GPS>(gb + 8 * kg, g0, kg, vec, bv[1]);
-                load_sb<GPS>(ub, g0, kg, vec, bv[2]);
-                load_sb<GPS>(ub + 8 * kg, g0, kg, vec, bv[3]);
-                float X[NT][2][GPS];
+            // x and its sums: one tile's are fetched a stage ahead (PRE), two tiles' for the whole stage at once
+            // or, where registers are short, sub-block by sub-block
+            constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
+            uint4 xv[NT][AHEAD ? Gm::SUBS * XV : XV];
+            float X[NT][2][GPS];
+            auto load_x = [&](int st, int sb, int at) {
+                const int k0 = st * Gm::SC + sb * Gm::KS;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) load_floats<GPS>(xs[t][q], st * GPS, ku, xvec, X[t][q]);
-                constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4;      // the whole stage's x in registers
-                uint4 xv[NT][AHEAD ? Gm::SUBS * XV : XV];
-                auto load_x = [&](int sb, int at) {
-                    const int k0 = st * Gm::SC + sb * Gm::KS;
+                    for (int v = 0; v < XV; ++v)
+                        xv[t][at + v] = __ldcg(reinterpret_cast<const uint4*>(xr[t] + k0) + v);
+            };
+            auto load_stage = [&](int st) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int v = 0; v < XV; ++v)
-                            xv[t][at + v] = k0 < a.K ? __ldcg(reinterpret_cast<const uint4*>(xr[t] + k0) + v) : make_uint4(0, 0, 0, 0);
-                };
+                    for (int q = 0; q < 2; ++q) load_floats<GPS>(xs[t][q] + st * GPS, X[t][q]);
                 if constexpr (AHEAD)
 #pragma unroll
-                    for (int sb = 0; sb < Gm::SUBS; ++sb) load_x(sb, sb * XV);
+                    for (int sb = 0; sb < Gm::SUBS; ++sb) load_x(st, sb, sb * XV);
+            };
+            if (PRE && nsw > 0) load_stage(s0);
+            if constexpr (!SHARED) wait_block(&sb_bar[warp], turn & 1, a.err);
+#pragma unroll 1
+            for (int s = 0; s < nsw; ++s) {
+                const int st = s0 + s * SSTEP;
+                if (!PRE) load_stage(st);
                 issue();
                 asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
                 __syncwarp();
                 const uint8_t* stage = ring + slot * STAGE + r * 64;
+                const uint8_t* sbp = ring + slot * STAGE + Gm::CODES + r * SBB;
+                const int g0 = st * Gm::SC / G;
+                uint4 xc[NT][AHEAD ? Gm::SUBS * XV : XV];
+                float Xc[NT][2][GPS];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int f = 0; f < GPS; ++f) Xc[t][q][f] = X[t][q][f];
+                if constexpr (AHEAD)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int v = 0; v < Gm::SUBS * XV; ++v) xc[t][v] = xv[t][v];
+                if (PRE && s + 1 < nsw) load_stage(st + SSTEP);
                 float d[2][NT][4];
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
-                    if constexpr (!AHEAD) load_x(sb, 0);
+                    if constexpr (!AHEAD) {
+                        load_x(st, sb, 0);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int v = 0; v < XV; ++v) xc[t][v] = xv[t][v];
+                    }
                     uint32_t fr[4][Gm::STEPS][2];
                     const int off = sb * 4 * Gm::LB + c * Gm::LB;
                     const uint8_t* wp = stage + (((off >> 4) ^ swz(r)) << 4) + (off & 15);
@@ -495,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xv[t][AHEAD ? sb * XV : 0]);
+                        const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xc[t][AHEAD ? sb * XV : 0]);
 #pragma unroll
                         for (int k = 0; k < Gm::STEPS; ++k)
 #pragma unroll
@@ -512,12 +585,23 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int m = i >> 1, h = i & 1;
-                            const float ss = sb_value<XT>(sv[i], f), bb = sb_value<XT>(bv[i], f);
+                            float ss, bb;
+                            if constexpr (SHARED) {
+                                uint32_t sv[SBB / 4], bv[SBB / 4];
+                                read_sb<SBB>(sbp + i * 8 * SBB, sv);
+                                read_sb<SBB>(sbp + ROWS * SBB + i * 8 * SBB, bv);
+                                ss = sb_value<GPS, XT>(sv, f, g0);
+                                bb = sb_value<GPS, XT>(bv, f, g0);
+                            } else {                     // past the last group: x is zero, any finite scale does
+                                const uint16_t* p = blk + (i * 8 + r) * kg + min(g0 + f, kg - 1);
+                                ss = half_bits_to_float(p[0], XT{});
+                                bb = half_bits_to_float(p[32 * kg], XT{});
+                            }
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
                                 for (int q = 0; q < 2; ++q)
-                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, X[t][q][f], acc[m][t][2 * h + q]));
+                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, Xc[t][q][f], acc[m][t][2 * h + q]));
                         }
                     }
                 }
@@ -527,6 +611,8 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
         };
         if (nt > 8) stages(std::integral_constant<int, 2>{});
         else stages(std::integral_constant<int, 1>{});
+        load_block(item + step);     // every lane has read this item's
+        ++turn;
 
         // ---- silu(gate) * up * weight, for columns r and r + 8 and tokens 2c, 2c + 1 of each tile ----
         if constexpr (SHARED) {      // the warps' slices of K together, in slice order, by the first warp's lanes
@@ -583,12 +669,17 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 
 // ---- down ----
 
-template <int BITS, typename XT, int G>
+// BLK: an entry's scales and biases come whole into one of two blocks that the CTA's warps share.
+template <int BITS, typename XT, int G, bool BLK>
 __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
     constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
+    constexpr int NST = Gm::NST, STAGE = Gm::stage(BLK), SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* yt = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);           // [WARPS][T][RP]
+    __shared__ uint64_t sb_full[2], sb_empty[2];
+    const int kg = a.N / G;
+    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(BLK));   // BLK: [2][scales, biases][ROWS][kg]
+    float* yt = reinterpret_cast<float*>(smem + Gm::ring(BLK) + (BLK ? 2 * 128 * kg : 0));   // [WARPS][T][RP]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
     const int cs = a.cs;
@@ -596,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
     const int row0 = (int)(blockIdx.x / cs) * ROWS;      // first column of y
 
     const int entries = __ldcg(a.entries);               // complete: the gate/up kernel waited for it before this one started
-    const int kg = a.N / G, nb_all = a.N / 16;
+    const int nb_all = a.N / 16;
     const int nst = (a.N + Gm::SC - 1) / Gm::SC;
     const int nsw = nst > warp ? (nst - warp + WARPS - 1) / WARPS : 0;
     const int row_bytes = a.N * BITS / 8;
@@ -605,6 +696,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 
     int l_ent = rank, l_s = 0, l_slot = 0, l_next = 0;
     const uint8_t* l_row[4] = {nullptr, nullptr, nullptr, nullptr};
+    const uint16_t *l_sc = nullptr, *l_bi = nullptr;     // of row `lane`
     if (l_ent < entries) l_next = __ldcg(a.entries + 1 + l_ent);
     auto issue = [&]() {
         if (l_ent < entries && nsw > 0) {
@@ -615,15 +707,21 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l_row[i] = wp + min(row0 + r + 8 * i, a.K - 1) * a.down.w_row * 4;
                 const int64_t so = (int64_t)min(row0 + lane, a.K - 1) * kg;
-                ptx::prefetch_l2(a.down.scales + e * a.down.s_exp + so);
-                ptx::prefetch_l2(a.down.biases + e * a.down.b_exp + so);
+                if constexpr (!BLK) {
+                    l_sc = a.down.scales + e * a.down.s_exp + so;
+                    l_bi = a.down.biases + e * a.down.b_exp + so;
+                }
             }
-            const int off = (warp + l_s * WARPS) * 64;
+            const int st = warp + l_s * WARPS, off = st * 64;
             const int size = off + c * 16 < row_bytes ? 16 : 0;
             const int o = size ? off : 0;
-            const uint32_t dst = ring_s + l_slot * STAGE + r * 64 + ((c ^ swz(r)) << 4);
+            const uint32_t slot0 = ring_s + l_slot * STAGE, dst = slot0 + r * 64 + ((c ^ swz(r)) << 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) cp16z(dst + i * 8 * 64, l_row[i] + o, size);
+            if constexpr (!BLK) {
+                copy_sb<GPS, SBB>(slot0 + Gm::CODES + lane * SBB, l_sc, st * Gm::SC / G, kg, a.down.svec);
+                copy_sb<GPS, SBB>(slot0 + Gm::CODES + (ROWS + lane) * SBB, l_bi, st * Gm::SC / G, kg, a.down.svec);
+            }
             if (++l_s == nsw) {
                 l_s = 0;
                 l_ent += cs;
@@ -634,6 +732,28 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
     };
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) issue();
+    if (BLK && threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sb_full[i], 1);
+            ptx::mbar_init(&sb_empty[i], WARPS);
+        }
+        ptx::fence_mbar_init();
+    }
+    // entry number i of this CTA into block i % 2: by one thread, once every warp has left the block's last entry
+    auto load_block = [&](int i) {
+        if constexpr (BLK) {
+            const int ent = rank + i * cs;
+            if (threadIdx.x == 0 && ent < entries) {
+                if (i >= 2) wait_block(&sb_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, a.err);
+                const int e = __ldcg(a.entries + 1 + ent) & 0xffff;
+                uint16_t* dst = blk + (i & 1) * 64 * kg;
+                ptx::mbar_arrive_expect_tx(&sb_full[i & 1], 128 * kg);
+                ptx::bulk_load(dst, a.down.scales + e * a.down.s_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
+                ptx::bulk_load(dst + 32 * kg, a.down.biases + e * a.down.b_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
+            }
+            __syncwarp();
+        }
+    };
     for (int i = threadIdx.x; i < WARPS * a.T * RP; i += THREADS) yt[i] = 0.0f;
     int next_ent = 0, next_pair = 0;
     auto fetch_entry = [&](int ent) {
@@ -643,15 +763,19 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
         }
     };
     fetch_entry(rank);
-    __syncthreads();             // the y tiles are zero
+    __syncthreads();             // the y tiles are zero, the barriers ready
+    load_block(0);
 
     ptx::pdl_wait();             // the activations
     ptx::pdl_launch_dependents();
 
-    int slot = 0;
+    int slot = 0, turn = 0;
     float* yw = yt + warp * a.T * RP;
-    for (int ent = rank; ent < entries; ent += cs) {
-        const int e = next_ent & 0xffff, nt = next_ent >> 16, pair = next_pair;
+    for (int ent = rank; ent < entries; ent += cs, ++turn) {
+        load_block(turn + 1);
+        if constexpr (BLK) wait_block(&sb_full[turn & 1], (uint32_t)(turn / 2) & 1, a.err);
+        const uint16_t* bk = blk + (turn & 1) * 64 * kg + r * kg;
+        const int nt = next_ent >> 16, pair = next_pair;
         fetch_entry(ent + cs);
         int po[2], px[2][2];     // rows of the workspace: token r of each tile; tokens 2c and 2c + 1
 #pragma unroll
@@ -660,10 +784,6 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 2; ++q) px[t][q] = __shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1));
         }
-        const uint16_t *sp = a.down.scales + e * a.down.s_exp, *bp = a.down.biases + e * a.down.b_exp;
-        int ro[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ro[i] = min(row0 + r + 8 * i, a.K - 1) * kg;
         float acc[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -677,13 +797,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 #pragma unroll 1
             for (int s = 0; s < nsw; ++s) {
                 const int st = warp + s * WARPS;
-                uint32_t sv[4][(GPS + 1) / 2], bv[4][(GPS + 1) / 2];
                 const int g0 = st * Gm::SC / G;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    load_sb<GPS>(sp + ro[i], g0, kg, a.down.svec, sv[i]);
-                    load_sb<GPS>(bp + ro[i], g0, kg, a.down.svec, bv[i]);
-                }
                 constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4;      // the whole stage's activations in registers
                 uint4 hv[NT][AHEAD ? Gm::SUBS * XV : XV];
                 float hs[NT][AHEAD ? Gm::SUBS : 1];                  // their power of two (this lane's 16)
@@ -705,6 +819,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
                 asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
                 __syncwarp();
                 const uint8_t* stage = ring + slot * STAGE + r * 64;
+                const uint8_t* sbp = ring + slot * STAGE + Gm::CODES + r * SBB;
                 float df[2][NT][4];                      // a fold's sum, in true units
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
@@ -767,14 +882,35 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
                             for (int q = 0; q < 2; ++q) {
                                 X[t][q] = 0.0f;
                                 const float* xp = a.hsum + (int64_t)px[t][q] * nb_all + x0;
-                                if (x0 < nb_all)
+                                // N is a multiple of the fold: rows and folds keep these loads aligned
+                                if (x0 < nb_all) {
+                                    if constexpr (Gm::FU == 32) {
+                                        const float2 u = __ldcg(reinterpret_cast<const float2*>(xp));
+                                        X[t][q] = u.x + u.y;
+                                    } else {
 #pragma unroll
-                                    for (int i = 0; i < Gm::FU / 16; ++i) X[t][q] += __ldcg(xp + i);
+                                        for (int i = 0; i < Gm::FU / 64; ++i) {
+                                            const float4 u = __ldcg(reinterpret_cast<const float4*>(xp) + i);
+                                            X[t][q] += (u.x + u.y) + (u.z + u.w);
+                                        }
+                                    }
+                                }
                             }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int m = i >> 1, h = i & 1;
-                            const float ss = sb_value<XT>(sv[i], f), bb = sb_value<XT>(bv[i], f);
+                            float ss, bb;
+                            if constexpr (BLK) {
+                                const uint16_t* p = bk + i * 8 * kg + min(g0 + f, kg - 1);
+                                ss = half_bits_to_float(p[0], XT{});
+                                bb = half_bits_to_float(p[32 * kg], XT{});
+                            } else {
+                                uint32_t sv[SBB / 4], bv[SBB / 4];
+                                read_sb<SBB>(sbp + i * 8 * SBB, sv);
+                                read_sb<SBB>(sbp + ROWS * SBB + i * 8 * SBB, bv);
+                                ss = sb_value<GPS, XT>(sv, f, g0);
+                                bb = sb_value<GPS, XT>(bv, f, g0);
+                            }
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -789,6 +925,10 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
         };
         if (nt > 8) stages(std::integral_constant<int, 2>{});
         else stages(std::integral_constant<int, 1>{});
+        if (BLK) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sb_empty[turn & 1]);
+        }
         // this warp's slice of N into its own tile of y
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -836,9 +976,12 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 
 template <int BITS, typename XT, int G>
 cudaError_t launch_t(const Args& a, cudaStream_t st) {
-    const size_t ring = (size_t)WARPS * NST * STAGE;
-    const size_t smem_shared = ring + 2 * WARPS * 16 * 32 * sizeof(float);
-    const size_t smem_down = ring + WARPS * a.T * RP * sizeof(float);
+    using Gm = Geo<BITS, G>;
+    const int kg = a.K / G, kgd = a.N / G;
+    const size_t smem_shared = Gm::ring(false) + 2 * WARPS * 16 * 32 * sizeof(float);
+    const size_t smem_own = Gm::ring(true) + (size_t)WARPS * 128 * kg;
+    const bool blk_down = a.down.blk && kgd <= DOWN_GROUPS;
+    const size_t smem_down = Gm::ring(blk_down) + (blk_down ? (size_t)2 * 128 * kgd : 0) + WARPS * a.T * RP * sizeof(float);
     constexpr int SMEM_MAX = 160 * 1024;
     static std::mutex mu;
     static bool done[64] = {false};
@@ -849,8 +992,8 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
-            const void* fns[3] = {(const void*)gate_up_kernel<BITS, XT, G, false>, (const void*)gate_up_kernel<BITS, XT, G, true>,
-                                  (const void*)down_kernel<BITS, XT, G>};
+            const void* fns[4] = {(const void*)gate_up_kernel<BITS, XT, G, false>, (const void*)gate_up_kernel<BITS, XT, G, true>,
+                                  (const void*)down_kernel<BITS, XT, G, false>, (const void*)down_kernel<BITS, XT, G, true>};
             for (const void* f : fns) {
                 e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
                 if (e != cudaSuccess) return e;
@@ -873,27 +1016,30 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     cfg.blockDim = dim3(32 * PREP_WARPS);
     e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT, G>, a);
     if (e != cudaSuccess) return e;
-    // as many items as the tokens could choose, at most what fits the device at once (four CTAs an SM); with
-    // fewer items than half the device's warps, four warps to an item
+    // As many items as the tokens could choose, at most what fits the device at once (four CTAs an SM).  With up
+    // to two items for every CTA that fits, four warps share an item: its latency counts, not the throughput (two
+    // tokens, 16 experts of 4 bits: 12.4 against 15.3 us; one token, 128 experts of 8 bits, over twice as many
+    // items: 58 against 54 us).  The same kernel takes rows whose scales do not fit a warp's block.
     const int64_t pairs = (int64_t)a.T * a.topk;
     const int64_t most = pairs < a.E + pairs / TB ? pairs : a.E + pairs / TB;
     const int64_t items = most * (a.N / 16), all = 148 * 4;
     cfg.blockDim = dim3(THREADS);
-    if (items * 2 <= all * WARPS) {
+    if (items <= 2 * all || kg > UP_GROUPS || !a.gate.blk || !a.up.blk) {
         cfg.gridDim = dim3((unsigned)(items < all ? items : all));
         cfg.dynamicSmemBytes = smem_shared;
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, true>, a);
     } else {
         const int64_t ctas = (items + WARPS - 1) / WARPS;
         cfg.gridDim = dim3((unsigned)(ctas < all ? ctas : all));
-        cfg.dynamicSmemBytes = ring;
+        cfg.dynamicSmemBytes = smem_own;
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, false>, a);
     }
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)((a.K + ROWS - 1) / ROWS * a.cs));
     cfg.dynamicSmemBytes = smem_down;
     cfg.numAttrs = a.cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G>, a);
+    return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true>, a)
+                    : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false>, a);
 }
 
 template <int BITS, typename XT>

@@ -598,13 +598,13 @@ aq_status check_bank(const aq_view* wq, const aq_view* sc, const aq_view* bi, co
     out->w_exp = E > 1 ? wq->stride[0] : 0;
     out->s_exp = E > 1 ? sc->stride[0] : 0;
     out->b_exp = E > 1 ? bi->stride[0] : 0;
-    // scales of a 64-byte stage (512 / bits codes) of a row as one aligned copy; a single one comes with a
+    // scales of 64 bytes (512 / bits codes) of a row as one aligned copy; a single one comes with a
     // neighbour, so rows have to hold an even number
     int64_t per = 512 / bits / group;
     if (per < 2) per = 2;
     out->svec = kg % per == 0 && (uintptr_t)sc->data % (2 * per) == 0 && (uintptr_t)bi->data % (2 * per) == 0 &&
                 out->s_exp % per == 0 && out->b_exp % per == 0;
-    out->blk = aligned16(sc->data) && aligned16(bi->data) && out->s_exp % 8 == 0 && out->b_exp % 8 == 0;
+    out->blk = out->svec && aligned16(sc->data) && aligned16(bi->data) && out->s_exp % 8 == 0 && out->b_exp % 8 == 0;
     return AQ_OK;
 }
 
@@ -1342,6 +1342,7 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
     a.entries = (int*)w;
     a.pairs = (uint16_t*)(w + lay.pairs);
     a.weight = (float*)(w + lay.weight);
+    a.hmax = (unsigned*)(w + lay.hmax);
     a.xh = (uint16_t*)(w + lay.xh);
     a.xsum = (float*)(w + lay.xsum);
     a.xfac = (float*)(w + lay.xfac);

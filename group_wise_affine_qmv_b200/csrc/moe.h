@@ -43,6 +43,7 @@ struct Args {
     // ... and by the gate/up kernel
     uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted
     float* hscale;              // [T * topk, N / 16]: those powers of two
+    unsigned* hmax;             // [T * topk]: the largest of each row's, as the bits of a float (zeroed by the first kernel)
     float* hsum;                // [T * topk, N / 16]: sums of 16 activations
     void* y;
     int64_t y_row;
@@ -57,19 +58,20 @@ struct Args {
 constexpr int TB = 16;          // tokens of an entry
 constexpr int MAX_ENTRIES = MAX_TOKENS * MAX_TOPK;
 
-// columns of prepared x, in whole stages of any width (2-bit stages hold 256 codes)
-__host__ __device__ constexpr int x_pitch(int K) { return (K + 255) / 256 * 256; }
+// columns of prepared x, in whole stages of any width (2-bit stages hold 512 codes)
+__host__ __device__ constexpr int x_pitch(int K) { return (K + 511) / 512 * 512; }
 
 // Offsets of the workspace's parts, each on a 16-byte boundary, and its size.  (Sums of x are kept per
 // 32 codes or more.)
 struct Layout {
-    size_t pairs, weight, xh, xsum, xfac, h, hscale, hsum, bytes;
+    size_t pairs, weight, hmax, xh, xsum, xfac, h, hscale, hsum, bytes;
     Layout(int64_t T, int64_t topk, int64_t K, int64_t N) {
         auto up = [](size_t v) { return (v + 15) / 16 * 16; };
         const size_t p = (size_t)T * topk;
         pairs = up((1 + MAX_ENTRIES) * sizeof(int));
         weight = pairs + up(p * TB * 2);
-        xh = weight + up(p * 4);
+        hmax = weight + up(p * 4);
+        xh = hmax + up(p * 4);
         xsum = xh + up((size_t)T * x_pitch((int)K) * 2);
         xfac = xsum + up((size_t)T * (x_pitch((int)K) / 32) * 4);
         h = xfac + up((size_t)T * 4);
@@ -82,7 +84,7 @@ struct Layout {
 // instantiated in kernels_moe_b<BITS>_<type>.cu
 template <int BITS, bool BF>
 cudaError_t launch_b(const Args& a, int group, cudaStream_t s);
-cudaError_t launch(Args& a, int bits, int group, bool bf16, cudaStream_t s);
+cudaError_t launch(const Args& a, int bits, int group, bool bf16, cudaStream_t s);
 
 }  // namespace moe
 }  // namespace aq

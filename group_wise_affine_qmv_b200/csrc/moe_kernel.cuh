@@ -17,7 +17,7 @@
 //    f16), its elements permuted and scaled to meet their codes' positions.
 //  - Sums of x per group come with it from the first kernel, so a group costs s D + b X, two FMAs per
 //    row and token.
-//  - A warp streams stages of 64 bytes x 32 weight rows through its own ring in shared memory with
+//  - A warp streams stages of 128 bytes x 32 weight rows through its own ring in shared memory with
 //    16-byte asynchronous copies; the ring runs on across items, so the next item's codes are in flight
 //    while one is finished.  Experts and token lists are fetched an item ahead.
 //  - Scales and biases of an item's rows are one dense run each, which a bulk copy brings whole.  (Copied
@@ -28,13 +28,17 @@
 //    does an item alone, all of K, and ends with both sums of an activation in one lane.  Where there
 //    are too few items to fill the device the four warps of a CTA share one, a quarter of the stages each.
 //  - The activations pass on as f16 with a power of two per 16 of them (11 bits of mantissa: y is rounded
-//    to 8 or 11), so the down kernel multiplies subnormal codes again.
+//    to 8 or 11), and the largest of a row's powers (an atomic maximum: order does not matter), on which the
+//    down kernel puts them, by one multiplication a pair, to multiply subnormal codes again.
+//  - x and its sums are read through L1: with few tokens all warps of the device walk the same lines, which
+//    from L2 cost up to 1.5 us a stage (one token: 53 against 42 us).
 //  - down: a CTA owns 32 columns of y for all tokens and walks the entries, its warps splitting N by
 //    stages; a cluster of up to eight CTAs splits the entries and adds its tiles in rank order.  It stages
 //    its first weights while the gate/up kernel still runs.  No atomics on results: nothing depends on
 //    timing.
 #pragma once
 
+#include <algorithm>
 #include <mutex>
 
 #include "moe.h"
@@ -53,21 +57,21 @@ constexpr uint64_t WAIT_NS = 2000000000ull;   // budget of a bounded wait
 
 template <int BITS, int G>
 struct Geo {
-    static constexpr int SC = 512 / BITS;                 // codes of a row per stage (64 bytes)
+    static constexpr int SC = 512 / BITS;                 // codes of a row per half stage (64 bytes)
     static constexpr int KS = G < 64 ? G : 64;            // codes per sub-block: a lane holds KS / 4 in a row
     static constexpr int SUBS = SC / KS;
     static constexpr int STEPS = KS / 16;
     static constexpr int LB = KS * BITS / 32;             // bytes of a row per lane and sub-block
-    static constexpr int FU = G < SC ? G : SC;            // codes per fold: a group, or a stage's part of it
+    static constexpr int FU = G < SC ? G : SC;            // codes per fold: a group, or a half stage's part of it
     static constexpr int SPF = FU / KS;
-    static constexpr int GPS = SC / FU;                   // folds per stage
-    // A stage in shared memory: codes, and where they come stage by stage the rows' scales and biases (the 4 or 8
-    // aligned bytes around its folds).
+    static constexpr int GPS = SC / FU;                   // folds per half stage
+    // A half stage in shared memory: codes, and where they come stage by stage the rows' scales and biases (the
+    // 4 or 8 aligned bytes around its folds).
     static constexpr int SBB = GPS == 4 ? 8 : 4;
     static constexpr int CODES = ROWS * 64;
-    static constexpr int stage(bool blk) { return CODES + (blk ? 0 : 2 * ROWS * SBB); }
-    static constexpr int NST = 4;                         // stages of a warp's ring
-    static constexpr int ring(bool blk) { return WARPS * NST * stage(blk); }
+    static constexpr int half(bool blk) { return CODES + (blk ? 0 : 2 * ROWS * SBB); }
+    static constexpr int NST = 3;                         // stages of a warp's ring
+    static constexpr int ring(bool blk) { return WARPS * NST * 2 * half(blk); }
     static_assert(LB >= 4, "a lane's codes fill whole words");
 };
 
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_cons
         return;
     }
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) R.mask[e] = 0;
+    for (int i = threadIdx.x; i < a.T * a.topk; i += blockDim.x) a.hmax[i] = 0;
     __syncthreads();
     if (a.E <= 128) route_tokens<4>(a, R, warp, lane);
     else route_tokens<MAX_EXPERTS / 32>(a, R, warp, lane);
@@ -327,7 +332,24 @@ __device__ __forceinline__ float sb_value(const uint32_t* v, int f, int g0) {
     const uint32_t w = v[f >> 1];
     return half_bits_to_float((uint16_t)((f & 1) ? w >> 16 : w), XT{});
 }
-// One scale (or bias) pair wait, bounded: on expiry the error word says so, and the results are void.
+// GPS values of a row of a block (rows hold a multiple of GPS, or of 2)
+template <int GPS>
+__device__ __forceinline__ void read_blk(const uint16_t* p, uint32_t (&v)[(GPS + 1) / 2]) {
+    if constexpr (GPS == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        v[0] = u.x; v[1] = u.y;
+    } else if constexpr (GPS == 2) {
+        v[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+        v[0] = *p;
+    }
+}
+template <int GPS, typename XT>
+__device__ __forceinline__ float blk_value(const uint32_t* v, int f) {
+    const uint32_t w = v[f >> 1];
+    return half_bits_to_float((uint16_t)((f & 1) ? w >> 16 : w), XT{});
+}
+// A wait for a block's copies, bounded: on expiry the error word says so, and the results are void.
 __device__ __forceinline__ void wait_block(uint64_t* bar, uint32_t parity, int* err) {
     volatile int never = 0;
     if (!ptx::mbar_wait(bar, parity, &never, WAIT_NS)) atomicOr(err, DEVERR_TIMEOUT);
@@ -344,13 +366,13 @@ __device__ __forceinline__ void read_sb(const uint8_t* p, uint32_t* v) {
 template <int N>
 __device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {   // aligned
     if constexpr (N == 4) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(p));
+        const float4 u = *reinterpret_cast<const float4*>(p);
         v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
     } else if constexpr (N == 2) {
-        const float2 u = __ldcg(reinterpret_cast<const float2*>(p));
+        const float2 u = *reinterpret_cast<const float2*>(p);
         v[0] = u.x; v[1] = u.y;
     } else {
-        v[0] = __ldcg(p);
+        v[0] = *p;
     }
 }
 
@@ -365,10 +387,10 @@ __device__ __forceinline__ float pow2_inverse(float v) { return __uint_as_float(
 
 // SHARED: the CTA's warps share an item, each a quarter of its stages; else a warp has items of its own.
 template <int BITS, typename XT, int G, bool SHARED>
-__global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
     constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
-    constexpr int NST = Gm::NST, STAGE = Gm::stage(!SHARED), SBB = Gm::SBB;
+    constexpr int NST = Gm::NST, HALF = Gm::half(!SHARED), STAGE = 2 * HALF, SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sb_bar[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
     const int nb_all = a.N / 16;
     const int items = __ldcg(a.entries) * nb_all;
     const int kp = x_pitch(a.K), ku = kp / Gm::FU;
-    const int nst = (a.K + Gm::SC - 1) / Gm::SC;
+    const int nst = (a.K + 2 * Gm::SC - 1) / (2 * Gm::SC);
     const int s0 = SHARED ? warp : 0;
     constexpr int SSTEP = SHARED ? WARPS : 1;
     const int nsw = nst > s0 ? (nst - s0 + SSTEP - 1) / SSTEP : 0;   // stages of this warp per item
@@ -423,17 +445,21 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                     ptx::prefetch_l2_bulk((lane < 2 ? B.scales + e * B.s_exp : B.biases + e * B.b_exp) + (int64_t)n0 * kg, 32 * kg);
                 }
             }
-            const int st = s0 + l_s * SSTEP, off = st * 64;
-            const int size = off + c * 16 < row_bytes ? 16 : 0;
-            const int o = size ? off : 0;
+            const int st = s0 + l_s * SSTEP, off = st * 128;
             const uint32_t slot0 = ring_s + l_slot * STAGE, dst = slot0 + r * 64 + ((c ^ swz(r)) << 4);
-            cp16z(dst, l_gate + o, size);
-            cp16z(dst + 8 * 64, l_gate + o + 32 * a.gate.w_row, size);
-            cp16z(dst + 16 * 64, l_up + o, size);
-            cp16z(dst + 24 * 64, l_up + o + 32 * a.up.w_row, size);
-            if constexpr (SHARED) {
-                copy_sb<GPS, SBB>(slot0 + Gm::CODES + lane * SBB, l_sc, st * Gm::SC / G, kg, a.gate.svec);
-                copy_sb<GPS, SBB>(slot0 + Gm::CODES + (ROWS + lane) * SBB, l_bi, st * Gm::SC / G, kg, a.gate.svec);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int size = off + hf * 64 + c * 16 < row_bytes ? 16 : 0;
+                const int o = size ? off + hf * 64 : 0;
+                cp16z(dst + hf * HALF, l_gate + o, size);
+                cp16z(dst + hf * HALF + 8 * 64, l_gate + o + 32 * a.gate.w_row, size);
+                cp16z(dst + hf * HALF + 16 * 64, l_up + o, size);
+                cp16z(dst + hf * HALF + 24 * 64, l_up + o + 32 * a.up.w_row, size);
+                if (SHARED && off + hf * 64 < row_bytes) {   // a half that K reaches: its folds are all there, or rows are not vec
+                    const int g = (2 * st + hf) * Gm::SC / G;
+                    copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + lane * SBB, l_sc, g, kg, a.gate.svec);
+                    copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + (ROWS + lane) * SBB, l_bi, g, kg, a.gate.svec);
+                }
             }
             if (++l_s == nsw) {
                 l_s = 0;
@@ -510,7 +536,7 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int v = 0; v < XV; ++v)
-                        xv[t][at + v] = __ldcg(reinterpret_cast<const uint4*>(xr[t] + k0) + v);
+                        xv[t][at + v] = reinterpret_cast<const uint4*>(xr[t] + k0)[v];
             };
             auto load_stage = [&](int st) {
 #pragma unroll
@@ -521,17 +547,20 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 #pragma unroll
                     for (int sb = 0; sb < Gm::SUBS; ++sb) load_x(st, sb, sb * XV);
             };
-            if (PRE && nsw > 0) load_stage(s0);
+            if (PRE && nsw > 0) load_stage(2 * s0);
             if constexpr (!SHARED) wait_block(&sb_bar[warp], turn & 1, a.err);
 #pragma unroll 1
             for (int s = 0; s < nsw; ++s) {
-                const int st = s0 + s * SSTEP;
+              issue();
+              asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+              __syncwarp();
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int st = 2 * (s0 + s * SSTEP) + hf;    // in halves
+                if (hf == 1 && st * Gm::SC >= a.K) break;    // K ends with the first half
                 if (!PRE) load_stage(st);
-                issue();
-                asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-                __syncwarp();
-                const uint8_t* stage = ring + slot * STAGE + r * 64;
-                const uint8_t* sbp = ring + slot * STAGE + Gm::CODES + r * SBB;
+                const uint8_t* stage = ring + slot * STAGE + hf * HALF + r * 64;
+                const uint8_t* sbp = ring + slot * STAGE + hf * HALF + Gm::CODES + r * SBB;
                 const int g0 = st * Gm::SC / G;
                 uint4 xc[NT][AHEAD ? Gm::SUBS * XV : XV];
                 float Xc[NT][2][GPS];
@@ -546,7 +575,16 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int v = 0; v < Gm::SUBS * XV; ++v) xc[t][v] = xv[t][v];
-                if (PRE && s + 1 < nsw) load_stage(st + SSTEP);
+                // (x is padded to whole stages: the half after this one is there, whether it counts or not)
+                if (PRE && (hf == 0 || s + 1 < nsw)) load_stage(hf == 0 ? st + 1 : st + 2 * SSTEP - 1);
+                [[maybe_unused]] uint32_t bs[4][(GPS + 1) / 2], bb_[4][(GPS + 1) / 2];    // scales and biases of rows r + 8 i
+                if constexpr (!SHARED) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        read_blk<GPS>(blk + (i * 8 + r) * kg + g0, bs[i]);
+                        read_blk<GPS>(blk + (i * 8 + r + 32) * kg + g0, bb_[i]);
+                    }
+                }
                 float d[2][NT][4];
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
@@ -592,10 +630,9 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                                 read_sb<SBB>(sbp + ROWS * SBB + i * 8 * SBB, bv);
                                 ss = sb_value<GPS, XT>(sv, f, g0);
                                 bb = sb_value<GPS, XT>(bv, f, g0);
-                            } else {                     // past the last group: x is zero, any finite scale does
-                                const uint16_t* p = blk + (i * 8 + r) * kg + min(g0 + f, kg - 1);
-                                ss = half_bits_to_float(p[0], XT{});
-                                bb = half_bits_to_float(p[32 * kg], XT{});
+                            } else {
+                                ss = blk_value<GPS, XT>(bs[i], f);
+                                bb = blk_value<GPS, XT>(bb_[i], f);
                             }
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
@@ -605,8 +642,9 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                         }
                     }
                 }
-                __syncwarp();
-                if (++slot == NST) slot = 0;
+              }
+              __syncwarp();
+              if (++slot == NST) slot = 0;
             }
         };
         if (nt > 8) stages(std::integral_constant<int, 2>{});
@@ -658,6 +696,7 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
                     hp[code_pos<BITS>(r + 8)] = float_to_half_bits(v1 * inv * code_scale<BITS>(r + 8), f16_t{});
                     if (r == 0) {
                         a.hscale[(int64_t)p * nb_all + nb] = sc;
+                        atomicMax(a.hmax + p, __float_as_uint(sc));
                         a.hsum[(int64_t)p * nb_all + nb] = sum;
                     }
                 }
@@ -671,10 +710,10 @@ __global__ void __launch_bounds__(THREADS, 4) gate_up_kernel(const __grid_consta
 
 // BLK: an entry's scales and biases come whole into one of two blocks that the CTA's warps share.
 template <int BITS, typename XT, int G, bool BLK>
-__global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
     constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
-    constexpr int NST = Gm::NST, STAGE = Gm::stage(BLK), SBB = Gm::SBB;
+    constexpr int NST = Gm::NST, HALF = Gm::half(BLK), STAGE = 2 * HALF, SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sb_full[2], sb_empty[2];
     const int kg = a.N / G;
@@ -688,7 +727,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 
     const int entries = __ldcg(a.entries);               // complete: the gate/up kernel waited for it before this one started
     const int nb_all = a.N / 16;
-    const int nst = (a.N + Gm::SC - 1) / Gm::SC;
+    const int nst = (a.N + 2 * Gm::SC - 1) / (2 * Gm::SC);
     const int nsw = nst > warp ? (nst - warp + WARPS - 1) / WARPS : 0;
     const int row_bytes = a.N * BITS / 8;
     uint8_t* ring = smem + warp * NST * STAGE;
@@ -712,15 +751,19 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
                     l_bi = a.down.biases + e * a.down.b_exp + so;
                 }
             }
-            const int st = warp + l_s * WARPS, off = st * 64;
-            const int size = off + c * 16 < row_bytes ? 16 : 0;
-            const int o = size ? off : 0;
+            const int st = warp + l_s * WARPS, off = st * 128;
             const uint32_t slot0 = ring_s + l_slot * STAGE, dst = slot0 + r * 64 + ((c ^ swz(r)) << 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cp16z(dst + i * 8 * 64, l_row[i] + o, size);
-            if constexpr (!BLK) {
-                copy_sb<GPS, SBB>(slot0 + Gm::CODES + lane * SBB, l_sc, st * Gm::SC / G, kg, a.down.svec);
-                copy_sb<GPS, SBB>(slot0 + Gm::CODES + (ROWS + lane) * SBB, l_bi, st * Gm::SC / G, kg, a.down.svec);
+            for (int hf = 0; hf < 2; ++hf) {
+                const int size = off + hf * 64 + c * 16 < row_bytes ? 16 : 0;
+                const int o = size ? off + hf * 64 : 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cp16z(dst + hf * HALF + i * 8 * 64, l_row[i] + o, size);
+                if (!BLK && off + hf * 64 < row_bytes) {
+                    const int g = (2 * st + hf) * Gm::SC / G;
+                    copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + lane * SBB, l_sc, g, kg, a.down.svec);
+                    copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + (ROWS + lane) * SBB, l_bi, g, kg, a.down.svec);
+                }
             }
             if (++l_s == nsw) {
                 l_s = 0;
@@ -777,12 +820,25 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
         const uint16_t* bk = blk + (turn & 1) * 64 * kg + r * kg;
         const int nt = next_ent >> 16, pair = next_pair;
         fetch_entry(ent + cs);
-        int po[2], px[2][2];     // rows of the workspace: token r of each tile; tokens 2c and 2c + 1
+        // rows of the workspace: token r of each tile (its activations and their powers of two, against the row's
+        // largest), tokens 2c and 2c + 1 (sums)
+        const uint16_t* hp[2];
+        const float *hsp[2], *xp[2][2];
+        float hinv[2], top[2][2];
+        int px[2][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            po[t] = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1));
+            const int po = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1));
+            hp[t] = a.h + (int64_t)po * a.N + c * (Gm::KS / 4);
+            hsp[t] = a.hscale + (int64_t)po * nb_all + c * (Gm::KS / 4) / 16;
+            const float mine = __uint_as_float(__ldcg(a.hmax + po));
+            hinv[t] = pow2_inverse(mine);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) px[t][q] = __shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1));
+            for (int q = 0; q < 2; ++q) {
+                px[t][q] = __shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1));
+                top[t][q] = __shfl_sync(0xffffffffu, mine, 8 * c + 4 * q);
+                xp[t][q] = a.hsum + (int64_t)px[t][q] * nb_all;
+            }
         }
         float acc[2][2][4];
 #pragma unroll
@@ -794,36 +850,100 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 
         auto stages = [&](auto tiles) {
             constexpr int NT = decltype(tiles)::value;
+            float xinv[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) xinv[t][q] = pow2_inverse(top[t][q]) * (1.0f / CODE);
+            // activations and their powers of two: one tile's are fetched half a stage ahead (PRE), two tiles' for the
+            // whole half at once or, where registers are short, sub-block by sub-block
+            constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
+            uint4 hv[NT][AHEAD ? Gm::SUBS * XV : XV];
+            float hs[NT][AHEAD ? Gm::SUBS : 1];
+            auto load_h = [&](int st, int sb, int at) {
+                const int k0 = st * Gm::SC + sb * Gm::KS;
+                if (!BLK && k0 >= a.N) return;       // (rows in blocks hold whole halves)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int v = 0; v < XV; ++v)
+                        hv[t][at * XV + v] = __ldcg(reinterpret_cast<const uint4*>(hp[t] + k0) + v);
+                    hs[t][at] = __ldcg(hsp[t] + k0 / 16);
+                }
+            };
+            auto load_half = [&](int st) {
+#pragma unroll
+                for (int sb = 0; sb < Gm::SUBS; ++sb) load_h(st, sb, AHEAD ? sb : 0);
+            };
+            if (PRE && nsw > 0) load_half(2 * warp);
 #pragma unroll 1
             for (int s = 0; s < nsw; ++s) {
-                const int st = warp + s * WARPS;
+              issue();
+              asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
+              __syncwarp();
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int st = 2 * (warp + s * WARPS) + hf;  // in halves
+                if (hf == 1 && st * Gm::SC >= a.N) break;
                 const int g0 = st * Gm::SC / G;
-                constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4;      // the whole stage's activations in registers
-                uint4 hv[NT][AHEAD ? Gm::SUBS * XV : XV];
-                float hs[NT][AHEAD ? Gm::SUBS : 1];                  // their power of two (this lane's 16)
-                auto load_h = [&](int sb, int at) {
-                    const int k0 = st * Gm::SC + sb * Gm::KS;
+                if (AHEAD && !PRE) load_half(st);
+                uint4 hc[NT][AHEAD ? Gm::SUBS * XV : XV];
+                float hsc[NT][AHEAD ? Gm::SUBS : 1];
+                if constexpr (AHEAD) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                        for (int v = 0; v < XV; ++v)
-                            hv[t][at * XV + v] = k0 < a.N ? __ldcg(reinterpret_cast<const uint4*>(a.h + (int64_t)po[t] * a.N + k0 + c * (Gm::KS / 4)) + v)
-                                                          : make_uint4(0, 0, 0, 0);
-                        hs[t][at] = k0 < a.N ? __ldcg(a.hscale + (int64_t)po[t] * nb_all + (k0 + c * (Gm::KS / 4)) / 16) : 0x1p-114f;
-                    }
-                };
-                if constexpr (AHEAD)
+                        for (int v = 0; v < Gm::SUBS * XV; ++v) hc[t][v] = hv[t][v];
 #pragma unroll
-                    for (int sb = 0; sb < Gm::SUBS; ++sb) load_h(sb, sb);
-                issue();
-                asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
-                __syncwarp();
-                const uint8_t* stage = ring + slot * STAGE + r * 64;
-                const uint8_t* sbp = ring + slot * STAGE + Gm::CODES + r * SBB;
-                float df[2][NT][4];                      // a fold's sum, in true units
+                        for (int v = 0; v < Gm::SUBS; ++v) hsc[t][v] = hs[t][v];
+                    }
+                }
+                if (PRE) {
+                    const int next = hf == 0 ? st + 1 : st + 2 * WARPS - 1;
+                    if (next * Gm::SC < a.N) load_half(next);
+                }
+                // sums of the half's activations by folds, as they are stored (16 by 16)
+                float4 xr4[NT][2][Gm::FU >= 64 ? GPS * (Gm::FU / 64) : 1];
+                float2 xr2[NT][2][Gm::FU == 32 ? GPS : 1];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        // N is a multiple of the fold: rows and folds keep these loads aligned
+                        const float* p = xp[t][q] + st * Gm::SC / 16;
+                        if constexpr (Gm::FU == 32) {
+#pragma unroll
+                            for (int f = 0; f < GPS; ++f)
+                                if (BLK || st * Gm::SC + f * Gm::FU < a.N) xr2[t][q][f] = __ldcg(reinterpret_cast<const float2*>(p) + f);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < GPS * (Gm::FU / 64); ++i)
+                                if (BLK || st * Gm::SC + i * 64 < a.N) xr4[t][q][i] = __ldcg(reinterpret_cast<const float4*>(p) + i);
+                        }
+                    }
+                const uint8_t* stage = ring + slot * STAGE + hf * HALF + r * 64;
+                const uint8_t* sbp = ring + slot * STAGE + hf * HALF + Gm::CODES + r * SBB;
+                [[maybe_unused]] uint32_t bs[4][(GPS + 1) / 2], bb_[4][(GPS + 1) / 2];    // scales and biases of rows r + 8 i
+                if constexpr (BLK) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        read_blk<GPS>(bk + i * 8 * kg + g0, bs[i]);
+                        read_blk<GPS>(bk + (i * 8 + 32) * kg + g0, bb_[i]);
+                    }
+                }
+                float d[2][NT][4];
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
-                    if constexpr (!AHEAD) load_h(sb, 0);
+                    if (!BLK && st * Gm::SC + sb * Gm::KS >= a.N) break;
+                    if constexpr (!AHEAD) {
+                        load_h(st, sb, 0);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                            for (int v = 0; v < XV; ++v) hc[t][v] = hv[t][v];
+                            hsc[t][0] = hs[t][0];
+                        }
+                    }
                     uint32_t fr[4][Gm::STEPS][2];
                     const int off = sb * 4 * Gm::LB + c * Gm::LB;
                     const uint8_t* wp = stage + (((off >> 4) ^ swz(r)) << 4) + (off & 15);
@@ -835,75 +955,50 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        // the sub-block's activations on the largest of its powers of two
-                        const float own = hs[t][AHEAD ? sb : 0];
-                        float top = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 2));
-                        if constexpr (Gm::KS == 64) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        const __half2 f = __float2half2_rn(own * pow2_inverse(top));
-                        uint32_t* hw = reinterpret_cast<uint32_t*>(&hv[t][AHEAD ? sb * XV : 0]);
+                        const __half2 f = __float2half2_rn(hsc[t][AHEAD ? sb : 0] * hinv[t]);
+                        uint32_t* hw = reinterpret_cast<uint32_t*>(&hc[t][AHEAD ? sb * XV : 0]);
 #pragma unroll
                         for (int k = 0; k < 4 * XV; ++k) {
                             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hw[k]), f);
                             hw[k] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        float d[2][4];
 #pragma unroll
                         for (int k = 0; k < Gm::STEPS; ++k)
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                if (k == 0)
-                                    mma0(d[m], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k], hw[2 * k + 1]);
+                                if (sb % Gm::SPF == 0 && k == 0)
+                                    mma0(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k], hw[2 * k + 1]);
                                 else
-                                    wm::mma16816<false>(d[m], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k],
-                                                        hw[2 * k + 1]);
-                            }
-                        // tokens 2c and 2c + 1 on their own power of two
-                        const float m0 = __shfl_sync(0xffffffffu, top, 8 * c) * CODE, m1 = __shfl_sync(0xffffffffu, top, 8 * c + 4) * CODE;
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (sb % Gm::SPF == 0) {
-                                    df[m][t][2 * h] = d[m][2 * h] * m0;
-                                    df[m][t][2 * h + 1] = d[m][2 * h + 1] * m1;
-                                } else {
-                                    df[m][t][2 * h] = fmaf(d[m][2 * h], m0, df[m][t][2 * h]);
-                                    df[m][t][2 * h + 1] = fmaf(d[m][2 * h + 1], m1, df[m][t][2 * h + 1]);
-                                }
+                                    wm::mma16816<false>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
+                                                        hw[2 * k], hw[2 * k + 1]);
                             }
                     }
                     if (sb % Gm::SPF == Gm::SPF - 1) {
                         const int f = sb / Gm::SPF;
-                        const int x0 = (st * Gm::SC + f * Gm::FU) / 16;
-                        float X[NT][2];
+                        float X[NT][2];          // in the units of the products
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                X[t][q] = 0.0f;
-                                const float* xp = a.hsum + (int64_t)px[t][q] * nb_all + x0;
-                                // N is a multiple of the fold: rows and folds keep these loads aligned
-                                if (x0 < nb_all) {
-                                    if constexpr (Gm::FU == 32) {
-                                        const float2 u = __ldcg(reinterpret_cast<const float2*>(xp));
-                                        X[t][q] = u.x + u.y;
-                                    } else {
+                                if constexpr (Gm::FU == 32) {
+                                    X[t][q] = xr2[t][q][f].x + xr2[t][q][f].y;
+                                } else {
+                                    X[t][q] = 0.0f;
 #pragma unroll
-                                        for (int i = 0; i < Gm::FU / 64; ++i) {
-                                            const float4 u = __ldcg(reinterpret_cast<const float4*>(xp) + i);
-                                            X[t][q] += (u.x + u.y) + (u.z + u.w);
-                                        }
+                                    for (int i = 0; i < Gm::FU / 64; ++i) {
+                                        const float4 u = xr4[t][q][f * (Gm::FU / 64) + i];
+                                        X[t][q] += (u.x + u.y) + (u.z + u.w);
                                     }
                                 }
+                                X[t][q] *= xinv[t][q];
                             }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int m = i >> 1, h = i & 1;
                             float ss, bb;
                             if constexpr (BLK) {
-                                const uint16_t* p = bk + i * 8 * kg + min(g0 + f, kg - 1);
-                                ss = half_bits_to_float(p[0], XT{});
-                                bb = half_bits_to_float(p[32 * kg], XT{});
+                                ss = blk_value<GPS, XT>(bs[i], f);
+                                bb = blk_value<GPS, XT>(bb_[i], f);
                             } else {
                                 uint32_t sv[SBB / 4], bv[SBB / 4];
                                 read_sb<SBB>(sbp + i * 8 * SBB, sv);
@@ -915,12 +1010,13 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
                                 for (int q = 0; q < 2; ++q)
-                                    acc[m][t][2 * h + q] = fmaf(ss, df[m][t][2 * h + q], fmaf(bb, X[t][q], acc[m][t][2 * h + q]));
+                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, X[t][q], acc[m][t][2 * h + q]));
                         }
                     }
                 }
-                __syncwarp();
-                if (++slot == NST) slot = 0;
+              }
+              __syncwarp();
+              if (++slot == NST) slot = 0;
             }
         };
         if (nt > 8) stages(std::integral_constant<int, 2>{});
@@ -939,7 +1035,7 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) yp[16 * m + 8 * h + r] += acc[m][t][2 * h + q];
+                        for (int h = 0; h < 2; ++h) yp[16 * m + 8 * h + r] += acc[m][t][2 * h + q] * CODE * top[t][q];
                 }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -975,13 +1071,18 @@ __global__ void __launch_bounds__(THREADS, 4) down_kernel(const __grid_constant_
 }
 
 template <int BITS, typename XT, int G>
-cudaError_t launch_t(const Args& a, cudaStream_t st) {
+cudaError_t launch_t(Args a, cudaStream_t st) {
     using Gm = Geo<BITS, G>;
     const int kg = a.K / G, kgd = a.N / G;
     const size_t smem_shared = Gm::ring(false) + 2 * WARPS * 16 * 32 * sizeof(float);
     const size_t smem_own = Gm::ring(true) + (size_t)WARPS * 128 * kg;
     const bool blk_down = a.down.blk && kgd <= DOWN_GROUPS;
     const size_t smem_down = Gm::ring(blk_down) + (blk_down ? (size_t)2 * 128 * kgd : 0) + WARPS * a.T * RP * sizeof(float);
+    // The down kernel's CTAs all at once on the device, one cluster of up to eight per 32 columns of y, no more
+    // CTAs in it than there can be entries (32 tokens, 128 experts: 352 CTAs where 296 fit took 600 us, 264 450 us).
+    const int blocks = (a.K + ROWS - 1) / ROWS;
+    const int fit = 148 * (int)std::min<size_t>(3, 227 * 1024 / (smem_down + 1024));
+    a.cs = std::max(1, std::min({8, fit / blocks, a.T * a.topk, a.E}));
     constexpr int SMEM_MAX = 160 * 1024;
     static std::mutex mu;
     static bool done[64] = {false};
@@ -1016,13 +1117,14 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     cfg.blockDim = dim3(32 * PREP_WARPS);
     e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT, G>, a);
     if (e != cudaSuccess) return e;
-    // As many items as the tokens could choose, at most what fits the device at once (four CTAs an SM).  With up
+    // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM).  With up
     // to two items for every CTA that fits, four warps share an item: its latency counts, not the throughput (two
     // tokens, 16 experts of 4 bits: 12.4 against 15.3 us; one token, 128 experts of 8 bits, over twice as many
     // items: 58 against 54 us).  The same kernel takes rows whose scales do not fit a warp's block.
     const int64_t pairs = (int64_t)a.T * a.topk;
     const int64_t most = pairs < a.E + pairs / TB ? pairs : a.E + pairs / TB;
-    const int64_t items = most * (a.N / 16), all = 148 * 4;
+    const int64_t items = most * (a.N / 16), all = 148 * 3;
+    bool full = items >= all;
     cfg.blockDim = dim3(THREADS);
     if (items <= 2 * all || kg > UP_GROUPS || !a.gate.blk || !a.up.blk) {
         cfg.gridDim = dim3((unsigned)(items < all ? items : all));
@@ -1030,6 +1132,7 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, true>, a);
     } else {
         const int64_t ctas = (items + WARPS - 1) / WARPS;
+        full = ctas >= all;
         cfg.gridDim = dim3((unsigned)(ctas < all ? ctas : all));
         cfg.dynamicSmemBytes = smem_own;
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, false>, a);
@@ -1038,6 +1141,12 @@ cudaError_t launch_t(const Args& a, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)((a.K + ROWS - 1) / ROWS * a.cs));
     cfg.dynamicSmemBytes = smem_down;
     cfg.numAttrs = a.cs > 1 ? 2 : 1;
+    // Early only next to a gate/up grid that leaves room: clusters that squeeze in between its last CTAs end up
+    // placed so that others have to wait for them (32 tokens, 128 experts: 680 us against 473).
+    if (full) {
+        cfg.attrs = attr + 1;
+        cfg.numAttrs -= 1;
+    }
     return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true>, a)
                     : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false>, a);
 }

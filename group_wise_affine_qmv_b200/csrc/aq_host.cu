@@ -1344,11 +1344,9 @@ AQ_API aq_status aq_moe_swiglu(const aq_view* x, const aq_view* logits, int top_
     a.weight = (float*)(w + lay.weight);
     a.hmax = (unsigned*)(w + lay.hmax);
     a.xh = (uint16_t*)(w + lay.xh);
-    a.xsum = (float*)(w + lay.xsum);
     a.xfac = (float*)(w + lay.xfac);
     a.h = (uint16_t*)(w + lay.h);
     a.hscale = (float*)(w + lay.hscale);
-    a.hsum = (float*)(w + lay.hsum);
     a.y = y->data;
     a.y_row = y->stride[0];
     a.ydt = y->dtype;

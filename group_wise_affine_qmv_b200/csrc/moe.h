@@ -38,13 +38,11 @@ struct Args {
     uint16_t* pairs;            // [MAX_ENTRIES][TB]: token * topk + choice of an entry's tokens
     float* weight;              // [T * topk]
     uint16_t* xh;               // [T, x_pitch(K)] f16: x scaled by a power of two per token, permuted like the codes
-    float* xsum;                // [T, x_pitch(K) / fold]: sums of xh over folds, in the codes' weight
     float* xfac;                // [T]: what takes the sums back (and the RMS norm)
     // ... and by the gate/up kernel
     uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted
     float* hscale;              // [T * topk, N / 16]: those powers of two
     unsigned* hmax;             // [T * topk]: the largest of each row's, as the bits of a float (zeroed by the first kernel)
-    float* hsum;                // [T * topk, N / 16]: sums of 16 activations
     void* y;
     int64_t y_row;
     int ydt;                    // DT of y
@@ -61,10 +59,9 @@ constexpr int MAX_ENTRIES = MAX_TOKENS * MAX_TOPK;
 // columns of prepared x, in whole stages of any width (2-bit stages hold 512 codes)
 __host__ __device__ constexpr int x_pitch(int K) { return (K + 511) / 512 * 512; }
 
-// Offsets of the workspace's parts, each on a 16-byte boundary, and its size.  (Sums of x are kept per
-// 32 codes or more.)
+// Offsets of the workspace's parts, each on a 16-byte boundary, and its size.
 struct Layout {
-    size_t pairs, weight, hmax, xh, xsum, xfac, h, hscale, hsum, bytes;
+    size_t pairs, weight, hmax, xh, xfac, h, hscale, bytes;
     Layout(int64_t T, int64_t topk, int64_t K, int64_t N) {
         auto up = [](size_t v) { return (v + 15) / 16 * 16; };
         const size_t p = (size_t)T * topk;
@@ -72,12 +69,10 @@ struct Layout {
         weight = pairs + up(p * TB * 2);
         hmax = weight + up(p * 4);
         xh = hmax + up(p * 4);
-        xsum = xh + up((size_t)T * x_pitch((int)K) * 2);
-        xfac = xsum + up((size_t)T * (x_pitch((int)K) / 32) * 4);
+        xfac = xh + up((size_t)T * x_pitch((int)K) * 2);
         h = xfac + up((size_t)T * 4);
         hscale = h + up(p * N * 2);
-        hsum = hscale + up(p * (N / 16) * 4);
-        bytes = hsum + up(p * (N / 16) * 4);
+        bytes = hscale + up(p * (N / 16) * 4);
     }
 };
 

@@ -15,8 +15,9 @@
 //    codes one AND and half a shift; the exact products and fp32 sums differ from those of the codes by
 //    powers of two only.  x is scaled by a power of two per token into f16's range (exact for bf16 and
 //    f16), its elements permuted and scaled to meet their codes' positions.
-//  - Sums of x per group come with it from the first kernel, so a group costs s D + b X, two FMAs per
-//    row and token.
+//  - A group costs s D + b X, two FMAs per row and token; X, the sum over the group, comes from one more MMA
+//    per k step whose codes are all one.  (Sums kept in memory by the kernel before and loaded per group took
+//    a third of the down kernel's time: 460 against 390 us for 32 tokens and 128 experts.)
 //  - A warp streams stages of 128 bytes x 32 weight rows through its own ring in shared memory with
 //    16-byte asynchronous copies; the ring runs on across items, so the next item's codes are in flight
 //    while one is finished.  Experts and token lists are fetched an item ahead.
@@ -109,6 +110,13 @@ __device__ __forceinline__ void expand(const uint32_t* w, uint32_t (*a)[2]) {
         }
     }
 }
+// the pairs of k step s as they are for codes of one
+template <int BITS>
+__device__ __forceinline__ void ones(int s, uint32_t& lo, uint32_t& hi) {
+    if constexpr (BITS == 8) lo = hi = 0x00010001u;
+    else if constexpr (BITS == 4) { lo = 0x00010001u; hi = 0x00100010u; }
+    else { lo = (s & 1) ? 0x00100010u : 0x00010001u; hi = (s & 1) ? 0x00400040u : 0x00040004u; }
+}
 constexpr float CODE = 0x1p24f;        // a code's weight in the sums
 
 __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -199,9 +207,8 @@ __device__ __forceinline__ void route_tokens(const Args& a, Routing& R, int warp
 }
 
 // Block 0 routes all tokens; block 1 + t prepares token t.
-template <int BITS, typename XT, int G>
+template <int BITS, typename XT>
 __global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_constant__ Args a) {
-    using Gm = Geo<BITS, G>;
     __shared__ Routing R;
     __shared__ float red[2][PREP_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -233,18 +240,11 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prep_kernel(const __grid_cons
         // 2^(14 - exponent of the largest value): exact products (an infinity's exponent stays in range)
         const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255) - 127, -100), 127);
         const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-        const int kp = x_pitch(a.K), ku = kp / Gm::FU;       // padded with zeros to whole stages
-        for (int u = warp; u < ku; u += PREP_WARPS) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < Gm::FU / 32; ++i) {
-                const int k = u * Gm::FU + lane + 32 * i, j = k & 15;
-                const float v = k < a.K ? half_bits_to_float(__ldcg(x + k), XT{}) * up : 0.0f;
-                sum += v;
-                a.xh[(int64_t)t * kp + (k & ~15) + code_pos<BITS>(j)] = float_to_half_bits(v * code_scale<BITS>(j), f16_t{});
-            }
-            sum = warp_sum(sum);
-            if (lane == 0) a.xsum[(int64_t)t * ku + u] = sum * (1.0f / CODE);
+        const int kp = x_pitch(a.K);         // padded with zeros to whole stages
+        for (int k = threadIdx.x; k < kp; k += blockDim.x) {
+            const int j = k & 15;
+            const float v = k < a.K ? half_bits_to_float(__ldcg(x + k), XT{}) * up : 0.0f;
+            a.xh[(int64_t)t * kp + (k & ~15) + code_pos<BITS>(j)] = float_to_half_bits(v * code_scale<BITS>(j), f16_t{});
         }
         if (threadIdx.x == 0) {
             const float norm = a.rms_eps > 0.0f ? rsqrtf(s2 / (float)a.K + a.rms_eps) : 1.0f;
@@ -363,16 +363,20 @@ __device__ __forceinline__ void read_sb(const uint8_t* p, uint32_t* v) {
         v[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
-template <int N>
-__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {   // aligned
-    if constexpr (N == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(p);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    } else if constexpr (N == 2) {
-        const float2 u = *reinterpret_cast<const float2*>(p);
-        v[0] = u.x; v[1] = u.y;
+// One k step of a tile: both row blocks' sums and the sum over the tokens' own values; `first` starts them.
+template <int BITS, int STEPS>
+__device__ __forceinline__ void mma_step(float (&d0)[4], float (&d1)[4], float (&X)[4], const uint32_t (&fr)[4][STEPS][2], int k,
+                                     const uint32_t* b, bool first) {
+    uint32_t lo, hi;
+    ones<BITS>(k, lo, hi);
+    if (first) {
+        mma0(d0, fr[0][k][0], fr[1][k][0], fr[0][k][1], fr[1][k][1], b[2 * k], b[2 * k + 1]);
+        mma0(d1, fr[2][k][0], fr[3][k][0], fr[2][k][1], fr[3][k][1], b[2 * k], b[2 * k + 1]);
+        mma0(X, lo, lo, hi, hi, b[2 * k], b[2 * k + 1]);
     } else {
-        v[0] = *p;
+        wm::mma16816<false>(d0, fr[0][k][0], fr[1][k][0], fr[0][k][1], fr[1][k][1], b[2 * k], b[2 * k + 1]);
+        wm::mma16816<false>(d1, fr[2][k][0], fr[3][k][0], fr[2][k][1], fr[3][k][1], b[2 * k], b[2 * k + 1]);
+        wm::mma16816<false>(X, lo, lo, hi, hi, b[2 * k], b[2 * k + 1]);
     }
 }
 
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
 
     const int nb_all = a.N / 16;
     const int items = __ldcg(a.entries) * nb_all;
-    const int kp = x_pitch(a.K), ku = kp / Gm::FU;
+    const int kp = x_pitch(a.K);
     const int nst = (a.K + 2 * Gm::SC - 1) / (2 * Gm::SC);
     const int s0 = SHARED ? warp : 0;
     constexpr int SSTEP = SHARED ? WARPS : 1;
@@ -504,17 +508,11 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
         const int nt = next_ent >> 16, pair = next_pair;
         const int nb = item % nb_all, n0 = nb * 16;
         fetch_item(item + step);
-        // this lane's x rows (token r of each tile; past the last one: the last one), and the sums of tokens 2c, 2c + 1
+        // this lane's x rows (token r of each tile; past the last one: the last one)
         const uint16_t* xr[2];
-        const float* xs[2][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int tok = __shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1)) / a.topk;
-            xr[t] = a.xh + (int64_t)tok * kp + c * (Gm::KS / 4);
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                xs[t][q] = a.xsum + (int64_t)(__shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1)) / a.topk) * ku;
-        }
+        for (int t = 0; t < 2; ++t)
+            xr[t] = a.xh + (int64_t)(__shfl_sync(0xffffffffu, pair, min(8 * t + r, nt - 1)) / a.topk) * kp + c * (Gm::KS / 4);
         float acc[2][2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -525,11 +523,10 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
 
         auto stages = [&](auto tiles) {
             constexpr int NT = decltype(tiles)::value;
-            // x and its sums: one tile's are fetched a stage ahead (PRE), two tiles' for the whole stage at once
-            // or, where registers are short, sub-block by sub-block
+            // x: one tile's is fetched half a stage ahead (PRE), two tiles' for the whole half at once or, where
+            // registers are short, sub-block by sub-block
             constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
             uint4 xv[NT][AHEAD ? Gm::SUBS * XV : XV];
-            float X[NT][2][GPS];
             auto load_x = [&](int st, int sb, int at) {
                 const int k0 = st * Gm::SC + sb * Gm::KS;
 #pragma unroll
@@ -538,16 +535,12 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                     for (int v = 0; v < XV; ++v)
                         xv[t][at + v] = reinterpret_cast<const uint4*>(xr[t] + k0)[v];
             };
-            auto load_stage = [&](int st) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) load_floats<GPS>(xs[t][q] + st * GPS, X[t][q]);
+            auto load_half = [&](int st) {
                 if constexpr (AHEAD)
 #pragma unroll
                     for (int sb = 0; sb < Gm::SUBS; ++sb) load_x(st, sb, sb * XV);
             };
-            if (PRE && nsw > 0) load_stage(2 * s0);
+            if (PRE && nsw > 0) load_half(2 * s0);
             if constexpr (!SHARED) wait_block(&sb_bar[warp], turn & 1, a.err);
 #pragma unroll 1
             for (int s = 0; s < nsw; ++s) {
@@ -558,25 +551,18 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
               for (int hf = 0; hf < 2; ++hf) {
                 const int st = 2 * (s0 + s * SSTEP) + hf;    // in halves
                 if (hf == 1 && st * Gm::SC >= a.K) break;    // K ends with the first half
-                if (!PRE) load_stage(st);
+                if (!PRE) load_half(st);
                 const uint8_t* stage = ring + slot * STAGE + hf * HALF + r * 64;
                 const uint8_t* sbp = ring + slot * STAGE + hf * HALF + Gm::CODES + r * SBB;
                 const int g0 = st * Gm::SC / G;
                 uint4 xc[NT][AHEAD ? Gm::SUBS * XV : XV];
-                float Xc[NT][2][GPS];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int f = 0; f < GPS; ++f) Xc[t][q][f] = X[t][q][f];
                 if constexpr (AHEAD)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int v = 0; v < Gm::SUBS * XV; ++v) xc[t][v] = xv[t][v];
                 // (x is padded to whole stages: the half after this one is there, whether it counts or not)
-                if (PRE && (hf == 0 || s + 1 < nsw)) load_stage(hf == 0 ? st + 1 : st + 2 * SSTEP - 1);
+                if (PRE && (hf == 0 || s + 1 < nsw)) load_half(hf == 0 ? st + 1 : st + 2 * SSTEP - 1);
                 [[maybe_unused]] uint32_t bs[4][(GPS + 1) / 2], bb_[4][(GPS + 1) / 2];    // scales and biases of rows r + 8 i
                 if constexpr (!SHARED) {
 #pragma unroll
@@ -585,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                         read_blk<GPS>(blk + (i * 8 + r + 32) * kg + g0, bb_[i]);
                     }
                 }
-                float d[2][NT][4];
+                float d[2][NT][4], X[NT][4];     // rows of X are alike: elements 0, 1 are those of tokens 2c, 2c + 1
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
                     if constexpr (!AHEAD) {
@@ -608,15 +594,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                     for (int t = 0; t < NT; ++t) {
                         const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xc[t][AHEAD ? sb * XV : 0]);
 #pragma unroll
-                        for (int k = 0; k < Gm::STEPS; ++k)
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                if (sb % Gm::SPF == 0 && k == 0)
-                                    mma0(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], xw[2 * k], xw[2 * k + 1]);
-                                else
-                                    wm::mma16816<false>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
-                                                        xw[2 * k], xw[2 * k + 1]);
-                            }
+                        for (int k = 0; k < Gm::STEPS; ++k) mma_step<BITS>(d[0][t], d[1][t], X[t], fr, k, xw, sb % Gm::SPF == 0 && k == 0);
                     }
                     if (sb % Gm::SPF == Gm::SPF - 1) {
                         const int f = sb / Gm::SPF;
@@ -638,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
                                 for (int q = 0; q < 2; ++q)
-                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, Xc[t][q][f], acc[m][t][2 * h + q]));
+                                    acc[m][t][2 * h + q] = fmaf(ss, d[m][t][2 * h + q], fmaf(bb, X[t][q], acc[m][t][2 * h + q]));
                         }
                     }
                 }
@@ -683,12 +661,9 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                 const float fac = __ldcg(a.xfac + p / a.topk), w = __ldcg(a.weight + p);
                 const float v0 = wm::silu(acc[0][t][q] * CODE * fac) * (acc[1][t][q] * CODE * fac) * w;
                 const float v1 = wm::silu(acc[0][t][2 + q] * CODE * fac) * (acc[1][t][2 + q] * CODE * fac) * w;
-                float m = fmaxf(fabsf(v0), fabsf(v1)), sum = v0 + v1;
+                float m = fmaxf(fabsf(v0), fabsf(v1));
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                }
+                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float sc = scale_for(m), inv = pow2_inverse(sc);
                 if (live) {
                     uint16_t* hp = a.h + (int64_t)p * a.N + n0;
@@ -697,7 +672,6 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                     if (r == 0) {
                         a.hscale[(int64_t)p * nb_all + nb] = sc;
                         atomicMax(a.hmax + p, __float_as_uint(sc));
-                        a.hsum[(int64_t)p * nb_all + nb] = sum;
                     }
                 }
             }
@@ -820,10 +794,10 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
         const uint16_t* bk = blk + (turn & 1) * 64 * kg + r * kg;
         const int nt = next_ent >> 16, pair = next_pair;
         fetch_entry(ent + cs);
-        // rows of the workspace: token r of each tile (its activations and their powers of two, against the row's
-        // largest), tokens 2c and 2c + 1 (sums)
+        // token r of each tile: its activations and their powers of two, against the row's largest; tokens 2c and
+        // 2c + 1: that largest
         const uint16_t* hp[2];
-        const float *hsp[2], *xp[2][2];
+        const float* hsp[2];
         float hinv[2], top[2][2];
         int px[2][2];
 #pragma unroll
@@ -837,7 +811,6 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
             for (int q = 0; q < 2; ++q) {
                 px[t][q] = __shfl_sync(0xffffffffu, pair, min(8 * t + 2 * c + q, nt - 1));
                 top[t][q] = __shfl_sync(0xffffffffu, mine, 8 * c + 4 * q);
-                xp[t][q] = a.hsum + (int64_t)px[t][q] * nb_all;
             }
         }
         float acc[2][2][4];
@@ -850,11 +823,6 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
 
         auto stages = [&](auto tiles) {
             constexpr int NT = decltype(tiles)::value;
-            float xinv[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) xinv[t][q] = pow2_inverse(top[t][q]) * (1.0f / CODE);
             // activations and their powers of two: one tile's are fetched half a stage ahead (PRE), two tiles' for the
             // whole half at once or, where registers are short, sub-block by sub-block
             constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
@@ -902,25 +870,6 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                     const int next = hf == 0 ? st + 1 : st + 2 * WARPS - 1;
                     if (next * Gm::SC < a.N) load_half(next);
                 }
-                // sums of the half's activations by folds, as they are stored (16 by 16)
-                float4 xr4[NT][2][Gm::FU >= 64 ? GPS * (Gm::FU / 64) : 1];
-                float2 xr2[NT][2][Gm::FU == 32 ? GPS : 1];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        // N is a multiple of the fold: rows and folds keep these loads aligned
-                        const float* p = xp[t][q] + st * Gm::SC / 16;
-                        if constexpr (Gm::FU == 32) {
-#pragma unroll
-                            for (int f = 0; f < GPS; ++f)
-                                if (BLK || st * Gm::SC + f * Gm::FU < a.N) xr2[t][q][f] = __ldcg(reinterpret_cast<const float2*>(p) + f);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < GPS * (Gm::FU / 64); ++i)
-                                if (BLK || st * Gm::SC + i * 64 < a.N) xr4[t][q][i] = __ldcg(reinterpret_cast<const float4*>(p) + i);
-                        }
-                    }
                 const uint8_t* stage = ring + slot * STAGE + hf * HALF + r * 64;
                 const uint8_t* sbp = ring + slot * STAGE + hf * HALF + Gm::CODES + r * SBB;
                 [[maybe_unused]] uint32_t bs[4][(GPS + 1) / 2], bb_[4][(GPS + 1) / 2];    // scales and biases of rows r + 8 i
@@ -931,7 +880,7 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                         read_blk<GPS>(bk + (i * 8 + 32) * kg + g0, bb_[i]);
                     }
                 }
-                float d[2][NT][4];
+                float d[2][NT][4], X[NT][4];
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) {
                     if (!BLK && st * Gm::SC + sb * Gm::KS >= a.N) break;
@@ -963,35 +912,10 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                             hw[k] = *reinterpret_cast<const uint32_t*>(&v);
                         }
 #pragma unroll
-                        for (int k = 0; k < Gm::STEPS; ++k)
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                if (sb % Gm::SPF == 0 && k == 0)
-                                    mma0(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1], hw[2 * k], hw[2 * k + 1]);
-                                else
-                                    wm::mma16816<false>(d[m][t], fr[2 * m][k][0], fr[2 * m + 1][k][0], fr[2 * m][k][1], fr[2 * m + 1][k][1],
-                                                        hw[2 * k], hw[2 * k + 1]);
-                            }
+                        for (int k = 0; k < Gm::STEPS; ++k) mma_step<BITS>(d[0][t], d[1][t], X[t], fr, k, hw, sb % Gm::SPF == 0 && k == 0);
                     }
                     if (sb % Gm::SPF == Gm::SPF - 1) {
                         const int f = sb / Gm::SPF;
-                        float X[NT][2];          // in the units of the products
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                if constexpr (Gm::FU == 32) {
-                                    X[t][q] = xr2[t][q][f].x + xr2[t][q][f].y;
-                                } else {
-                                    X[t][q] = 0.0f;
-#pragma unroll
-                                    for (int i = 0; i < Gm::FU / 64; ++i) {
-                                        const float4 u = xr4[t][q][f * (Gm::FU / 64) + i];
-                                        X[t][q] += (u.x + u.y) + (u.z + u.w);
-                                    }
-                                }
-                                X[t][q] *= xinv[t][q];
-                            }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int m = i >> 1, h = i & 1;
@@ -1115,7 +1039,7 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)(1 + a.T));
     cfg.blockDim = dim3(32 * PREP_WARPS);
-    e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT, G>, a);
+    e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT>, a);
     if (e != cudaSuccess) return e;
     // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM).  With up
     // to two items for every CTA that fits, four warps share an item: its latency counts, not the throughput (two

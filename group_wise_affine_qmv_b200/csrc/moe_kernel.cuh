@@ -71,8 +71,10 @@ struct Geo {
     static constexpr int SBB = GPS == 4 ? 8 : 4;
     static constexpr int CODES = ROWS * 64;
     static constexpr int half(bool blk) { return CODES + (blk ? 0 : 2 * ROWS * SBB); }
-    static constexpr int NST = 3;                         // stages of a warp's ring
-    static constexpr int ring(bool blk) { return WARPS * NST * 2 * half(blk); }
+    // Stages of a warp's ring.  The down kernel's is short for a third CTA on an SM next to the tiles of y (32 tokens,
+    // 128 experts of 8 bits: 428 us the layer with 3 stages, two CTAs, 393 with 2; where three fit anyway: alike).
+    static constexpr int NST = 3, NST_DOWN = 2;
+    static constexpr int ring(int stages, bool blk) { return WARPS * stages * 2 * half(blk); }
     static_assert(LB >= 4, "a lane's codes fill whole words");
 };
 
@@ -402,9 +404,9 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
     const int kg = a.K / G;
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_s = ptx::smem_u32(ring);
-    float* red = reinterpret_cast<float*>(smem + Gm::ring(false));   // SHARED: [2][WARPS][16][32]
+    float* red = reinterpret_cast<float*>(smem + Gm::ring(Gm::NST, false));   // SHARED: [2][WARPS][16][32]
     // not SHARED: this warp's item's scales and biases, [gate s, up s, gate b, up b][16 rows][kg]
-    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(true)) + warp * 64 * kg;
+    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(Gm::NST, true)) + warp * 64 * kg;
     if (!SHARED) {
         if (lane == 0) ptx::mbar_init(&sb_bar[warp], 1);
         ptx::fence_mbar_init();
@@ -687,12 +689,13 @@ template <int BITS, typename XT, int G, bool BLK>
 __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
     constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
-    constexpr int NST = Gm::NST, HALF = Gm::half(BLK), STAGE = 2 * HALF, SBB = Gm::SBB;
+    constexpr int NST = Gm::NST_DOWN, HALF = Gm::half(BLK), STAGE = 2 * HALF, SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t sb_full[2], sb_empty[2];
+    __shared__ uint64_t sb_full[2];
+    __shared__ int sb_left[2];       // warps that have left a block's entry
     const int kg = a.N / G;
-    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(BLK));   // BLK: [2][scales, biases][ROWS][kg]
-    float* yt = reinterpret_cast<float*>(smem + Gm::ring(BLK) + (BLK ? 2 * 128 * kg : 0));   // [WARPS][T][RP]
+    uint16_t* blk = reinterpret_cast<uint16_t*>(smem + Gm::ring(NST, BLK));   // BLK: [2][scales, biases][ROWS][kg]
+    float* yt = reinterpret_cast<float*>(smem + Gm::ring(NST, BLK) + (BLK ? 2 * 128 * kg : 0));   // [WARPS][T][RP]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
     const int cs = a.cs;
@@ -702,20 +705,30 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
     const int entries = __ldcg(a.entries);               // complete: the gate/up kernel waited for it before this one started
     const int nb_all = a.N / 16;
     const int nst = (a.N + 2 * Gm::SC - 1) / (2 * Gm::SC);
-    const int nsw = nst > warp ? (nst - warp + WARPS - 1) / WARPS : 0;
     const int row_bytes = a.N * BITS / 8;
     uint8_t* ring = smem + warp * NST * STAGE;
     const uint32_t ring_s = ptx::smem_u32(ring);
 
-    int l_ent = rank, l_s = 0, l_slot = 0, l_next = 0;
+    // The CTA's entries are one row of stages, dealt to the warps in turn: with each entry dealt anew, 6 stages an
+    // entry left two of the four warps waiting half of the time.
+    int l_ent = rank, l_s = warp, l_slot = 0, l_next = 0;
+    bool l_new = true;
+    auto settle = [&]() {        // the entry that the next stage is in, and its expert
+        while (l_s >= nst && l_ent < entries) {
+            l_s -= nst;
+            l_ent += cs;
+            l_new = true;
+        }
+        if (l_new && l_ent < entries) l_next = __ldcg(a.entries + 1 + l_ent);
+    };
     const uint8_t* l_row[4] = {nullptr, nullptr, nullptr, nullptr};
     const uint16_t *l_sc = nullptr, *l_bi = nullptr;     // of row `lane`
-    if (l_ent < entries) l_next = __ldcg(a.entries + 1 + l_ent);
+    settle();
     auto issue = [&]() {
-        if (l_ent < entries && nsw > 0) {
-            if (l_s == 0) {
+        if (l_ent < entries) {
+            if (l_new) {
+                l_new = false;
                 const int e = l_next & 0xffff;
-                if (l_ent + cs < entries) l_next = __ldcg(a.entries + 1 + l_ent + cs);
                 const uint8_t* wp = reinterpret_cast<const uint8_t*>(a.down.wq + e * a.down.w_exp) + c * 16;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l_row[i] = wp + min(row0 + r + 8 * i, a.K - 1) * a.down.w_row * 4;
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                     l_bi = a.down.biases + e * a.down.b_exp + so;
                 }
             }
-            const int st = warp + l_s * WARPS, off = st * 128;
+            const int off = l_s * 128;
             const uint32_t slot0 = ring_s + l_slot * STAGE, dst = slot0 + r * 64 + ((c ^ swz(r)) << 4);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -734,15 +747,13 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cp16z(dst + hf * HALF + i * 8 * 64, l_row[i] + o, size);
                 if (!BLK && off + hf * 64 < row_bytes) {
-                    const int g = (2 * st + hf) * Gm::SC / G;
+                    const int g = (2 * l_s + hf) * Gm::SC / G;
                     copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + lane * SBB, l_sc, g, kg, a.down.svec);
                     copy_sb<GPS, SBB>(slot0 + hf * HALF + Gm::CODES + (ROWS + lane) * SBB, l_bi, g, kg, a.down.svec);
                 }
             }
-            if (++l_s == nsw) {
-                l_s = 0;
-                l_ent += cs;
-            }
+            l_s += WARPS;
+            settle();
             if (++l_slot == NST) l_slot = 0;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -752,24 +763,16 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
     if (BLK && threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sb_full[i], 1);
-            ptx::mbar_init(&sb_empty[i], WARPS);
+            sb_left[i] = 0;
         }
         ptx::fence_mbar_init();
     }
-    // entry number i of this CTA into block i % 2: by one thread, once every warp has left the block's last entry
-    auto load_block = [&](int i) {
-        if constexpr (BLK) {
-            const int ent = rank + i * cs;
-            if (threadIdx.x == 0 && ent < entries) {
-                if (i >= 2) wait_block(&sb_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, a.err);
-                const int e = __ldcg(a.entries + 1 + ent) & 0xffff;
-                uint16_t* dst = blk + (i & 1) * 64 * kg;
-                ptx::mbar_arrive_expect_tx(&sb_full[i & 1], 128 * kg);
-                ptx::bulk_load(dst, a.down.scales + e * a.down.s_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
-                ptx::bulk_load(dst + 32 * kg, a.down.biases + e * a.down.b_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
-            }
-            __syncwarp();
-        }
+    // entry number i of this CTA, of expert e, into block i % 2: by one thread, once every warp has left the block
+    auto load_block = [&](int i, int e) {
+        uint16_t* dst = blk + (i & 1) * 64 * kg;
+        ptx::mbar_arrive_expect_tx(&sb_full[i & 1], 128 * kg);
+        ptx::bulk_load(dst, a.down.scales + e * a.down.s_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
+        ptx::bulk_load(dst + 32 * kg, a.down.biases + e * a.down.b_exp + (int64_t)row0 * kg, 64 * kg, &sb_full[i & 1]);
     };
     for (int i = threadIdx.x; i < WARPS * a.T * RP; i += THREADS) yt[i] = 0.0f;
     int next_ent = 0, next_pair = 0;
@@ -781,15 +784,19 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
     };
     fetch_entry(rank);
     __syncthreads();             // the y tiles are zero, the barriers ready
-    load_block(0);
+    if (BLK && threadIdx.x == 0)
+        for (int i = 0; i < 2; ++i)
+            if (rank + i * cs < entries) load_block(i, __ldcg(a.entries + 1 + rank + i * cs) & 0xffff);
+    __syncwarp();
 
     ptx::pdl_wait();             // the activations
     ptx::pdl_launch_dependents();
 
-    int slot = 0, turn = 0;
+    int slot = 0, turn = 0, s0 = warp;   // s0: this warp's next stage, in the current entry
     float* yw = yt + warp * a.T * RP;
     for (int ent = rank; ent < entries; ent += cs, ++turn) {
-        load_block(turn + 1);
+        int after = 0;               // the entry that this one's block takes next
+        if constexpr (BLK) if (ent + 2 * cs < entries) after = __ldcg(a.entries + 1 + ent + 2 * cs);
         if constexpr (BLK) wait_block(&sb_full[turn & 1], (uint32_t)(turn / 2) & 1, a.err);
         const uint16_t* bk = blk + (turn & 1) * 64 * kg + r * kg;
         const int nt = next_ent >> 16, pair = next_pair;
@@ -835,23 +842,23 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
                     for (int v = 0; v < XV; ++v)
-                        hv[t][at * XV + v] = __ldcg(reinterpret_cast<const uint4*>(hp[t] + k0) + v);
-                    hs[t][at] = __ldcg(hsp[t] + k0 / 16);
+                        hv[t][at * XV + v] = reinterpret_cast<const uint4*>(hp[t] + k0)[v];
+                    hs[t][at] = hsp[t][k0 / 16];
                 }
             };
             auto load_half = [&](int st) {
 #pragma unroll
                 for (int sb = 0; sb < Gm::SUBS; ++sb) load_h(st, sb, AHEAD ? sb : 0);
             };
-            if (PRE && nsw > 0) load_half(2 * warp);
+            if (PRE) load_half(2 * s0);
 #pragma unroll 1
-            for (int s = 0; s < nsw; ++s) {
+            for (; s0 < nst; s0 += WARPS) {
               issue();
               asm volatile("cp.async.wait_group %0;" ::"n"(NST - 1) : "memory");
               __syncwarp();
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
-                const int st = 2 * (warp + s * WARPS) + hf;  // in halves
+                const int st = 2 * s0 + hf;  // in halves
                 if (hf == 1 && st * Gm::SC >= a.N) break;
                 const int g0 = st * Gm::SC / G;
                 if (AHEAD && !PRE) load_half(st);
@@ -943,18 +950,30 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
               if (++slot == NST) slot = 0;
             }
         };
-        if (nt > 8) stages(std::integral_constant<int, 2>{});
-        else stages(std::integral_constant<int, 1>{});
-        if (BLK) {
+        const bool any = s0 < nst;
+        if (any) {
+            if (nt > 8) stages(std::integral_constant<int, 2>{});
+            else stages(std::integral_constant<int, 1>{});
+        }
+        s0 -= nst;
+        if constexpr (BLK) {         // the last warp to leave has it filled again
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sb_empty[turn & 1]);
+            if (lane == 0 && ent + 2 * cs < entries) {
+                int left;
+                asm volatile("atom.acq_rel.cta.shared.add.s32 %0, [%1], 1;" : "=r"(left) : "r"(ptx::smem_u32(&sb_left[turn & 1])) : "memory");
+                if (left == WARPS - 1) {
+                    sb_left[turn & 1] = 0;
+                    load_block(turn + 2, after & 0xffff);
+                }
+            }
+            __syncwarp();
         }
         // this warp's slice of N into its own tile of y
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                if (8 * t + 2 * c + q < nt) {
+                if (any && 8 * t + 2 * c + q < nt) {
                     float* yp = yw + (px[t][q] / a.topk) * RP;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
@@ -998,10 +1017,10 @@ template <int BITS, typename XT, int G>
 cudaError_t launch_t(Args a, cudaStream_t st) {
     using Gm = Geo<BITS, G>;
     const int kg = a.K / G, kgd = a.N / G;
-    const size_t smem_shared = Gm::ring(false) + 2 * WARPS * 16 * 32 * sizeof(float);
-    const size_t smem_own = Gm::ring(true) + (size_t)WARPS * 128 * kg;
+    const size_t smem_shared = Gm::ring(Gm::NST, false) + 2 * WARPS * 16 * 32 * sizeof(float);
+    const size_t smem_own = Gm::ring(Gm::NST, true) + (size_t)WARPS * 128 * kg;
     const bool blk_down = a.down.blk && kgd <= DOWN_GROUPS;
-    const size_t smem_down = Gm::ring(blk_down) + (blk_down ? (size_t)2 * 128 * kgd : 0) + WARPS * a.T * RP * sizeof(float);
+    const size_t smem_down = Gm::ring(Gm::NST_DOWN, blk_down) + (blk_down ? (size_t)2 * 128 * kgd : 0) + WARPS * a.T * RP * sizeof(float);
     // The down kernel's CTAs all at once on the device, one cluster of up to eight per 32 columns of y, no more
     // CTAs in it than there can be entries (32 tokens, 128 experts: 352 CTAs where 296 fit took 600 us, 264 450 us).
     const int blocks = (a.K + ROWS - 1) / ROWS;

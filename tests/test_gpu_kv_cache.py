@@ -231,6 +231,33 @@ def test_attention_long_contexts_are_split_and_repeat_bit_for_bit():
         assert torch.equal(a, _run(q, kc, vc, pages, n, group))
 
 
+def test_attention_many_sequences_share_the_ctas():
+    """More items than CTAs, lengths from nothing to several pages: CTAs begin and end inside items."""
+    g = torch.Generator().manual_seed(5)
+    for B, Hq, H, D, group, S, Tq, window in ((70, 16, 8, 128, 64, 16, 1, 0), (150, 8, 4, 64, 32, 8, 2, 0),
+                                              (97, 20, 5, 256, 128, 32, 3, 40)):
+        lengths = torch.randint(0, 300, (B,), generator=g).tolist()
+        lengths[3], lengths[7] = 0, 1
+        q, kc, vc, pages, n = _case(B, Hq, H, D, group, S, Tq, lengths, BF, seed=8)
+        a = _run(q, kc, vc, pages, n, group, window=window)
+        _close(a, *ref.attention(q, kc, vc, pages, n, group, D ** -0.5, window))
+        assert torch.equal(a, _run(q, kc, vc, pages, n, group, window=window))
+
+
+def test_attention_a_warp_walks_many_tiles():
+    """Contexts so long that every warp of a full device has more tiles than it fetches page numbers for at once; the
+    pages repeat, which keeps the cache small."""
+    B, Hq, H, D, group, S = 2, 16, 8, 64, 64, 16
+    lengths = [130001, 120007]
+    kc = ref.make_cache(64, H, S, D, group, F16, 31)
+    vc = ref.make_cache(64, H, S, D, group, F16, 32)
+    g = torch.Generator().manual_seed(33)
+    pages = torch.randint(0, 64, (B, -(-max(lengths) // S)), generator=g)
+    q = inputs.normal((B, 1, Hq, D), 1.0, F16, seed=34)
+    n = torch.tensor(lengths)
+    _close(_run(q, kc, vc, pages, n, group), *ref.attention(q, kc, vc, pages, n, group, D ** -0.5))
+
+
 def test_attention_ignores_what_lies_behind_a_sequence():
     """Stale slots of the last page with NaN and infinite scales, pages past the end, other sequences' pages."""
     q, kc, vc, pages, n = _case(2, 4, 2, 128, 64, 16, 3, [37, 2], BF, seed=7)

@@ -1,12 +1,12 @@
 """GPU tests of the mixture-of-experts layer (aq_moe_swiglu) against the formula in 64 bits.
 
 Tolerance.  y = r + sum_j w_j Wd (silu(g) u), all sums fp32.  Rounding y is half a step of its type.  g and u are sums of
-K products whose codes carry an offset of at most 128 (removed through the group sums): each is off by at most
+K products, s D + b X per group (D sums codes times x, X sums x): each is off by at most
 e1 = 2^-19 sum_k |n x_k| (|s| (128 + code) + |b|) (MMAs of 16 products, at most 8 a group, each within 2^-23 of the
 magnitudes summed, and the folds of K/G groups over four warps, 2^-24 each of at most 2^4 of them one after another).
 h = w silu(g) u is off by |w| (|u| 1.1 e1 + |silu(g)| e1) (|silu'| <= 1.1); it is carried as f16 with a power of two per 16
-values (per 64 when multiplied), off by half a step of 11 bits, 2^-11 |h|, or where it is a subnormal by 2^-25 / 2^13 = 2^-38
-of the largest of its row; __expf and the divisions are within 2^-18 of h.  The down product adds 2^-19 sum |h| (|s| (128 + code) + |b|) and weighs
+values (per row when multiplied), off by half a step of 11 bits, 2^-11 |h|, or where it is a subnormal by 2^-25 / 2^13 = 2^-38
+of the largest of its row times the code's weight, at most 2^6: 2^-32; __expf and the divisions are within 2^-18 of h.  The down product adds 2^-19 sum |h| (|s| (128 + code) + |b|) and weighs
 the errors of h with |Wd|.
 """
 import numpy as np
@@ -57,7 +57,7 @@ def reference(x, logits, top_k, banks, norm, rms_eps, r, ydt):
             eg, eu = (2.0 ** -19 * (m.mag[e] @ xt.abs()) for m in (gate, up))
             s = g * torch.sigmoid(g)
             h = we * s * u
-            eh = we * (u.abs() * 1.1 * eg + s.abs() * eu + eg * eu) + (2.0 ** -11 + 2.0 ** -18) * h.abs() + 2.0 ** -38 * h.abs().max()
+            eh = we * (u.abs() * 1.1 * eg + s.abs() * eu + eg * eu) + (2.0 ** -11 + 2.0 ** -18) * h.abs() + 2.0 ** -32 * h.abs().max()
             y[t] += down.v[e] @ h
             err[t] += down.v[e].abs() @ eh + 2.0 ** -19 * (down.mag[e] @ (h.abs() + eh))
     u = torch.finfo(ydt).eps / 2
@@ -102,6 +102,31 @@ def test_layer_matches_the_formula(T, E, top_k, K, N, group, bits, dtype, norm, 
     r = inputs.normal((T, K), 1.0, ydt, seed=99) if res else None
     y = call(banks, x, logits, top_k, group, bits, norm_topk=norm, rms_eps=rms, residual=r, out_dtype=ydt)
     close(y, *reference(x, logits, top_k, banks, norm, rms, r, ydt))
+
+
+@pytest.mark.parametrize("T,E,top_k,K,N,group,bits,dtype", [
+    (40, 64, 4, 256, 512, 64, 4, BF),       # more than two gate/up items per CTA that fits: a warp has items of its own
+    (64, 8, 2, 160, 1024, 32, 8, F16),      # the same with 16 tokens an entry and rows of odd numbers of groups
+    (48, 40, 3, 192, 512, 64, 2, BF),
+    (64, 4, 2, 2112, 1216, 32, 4, BF),      # rows whose scales do not fit a warp's block
+    (64, 4, 2, 96, 8224, 32, 8, BF),        # and those of the down bank
+    (30, 32, 4, 384, 640, 128, 8, F16),
+])
+def test_many_items(T, E, top_k, K, N, group, bits, dtype):
+    banks, x, logits = setup(T, E, K, N, group, bits, dtype, seed=T + K)
+    y = call(banks, x, logits, top_k, group, bits, out_dtype=F32)
+    close(y, *reference(x, logits, top_k, banks, True, 0.0, None, F32))
+    # scales and biases one element past a 16-byte boundary
+    odd = []
+    for b in banks:
+        wq, *sb = b.dev
+        flat = [torch.zeros(t.numel() + 1, dtype=t.dtype, device=DEV) for t in sb]
+        for f, t in zip(flat, sb):
+            f[1:] = t.flatten()
+        odd.append((wq, *[f[1:].view(t.shape) for f, t in zip(flat, sb)]))
+    z = aq.aq_moe_swiglu(x.to(DEV), logits.to(DEV), top_k, *odd, group, bits, out_dtype=F32)
+    aq.aq_device_error()
+    close(z, *reference(x, logits, top_k, banks, True, 0.0, None, F32))
 
 
 def test_ties_infinities_and_empty_rows():

@@ -1,9 +1,10 @@
 // kernels_kv_append.cu -- new keys and values into the 4-bit paged cache.
 //
-// Per token, head and group of G elements, the quantizer of kernels_quant.cu bit for bit, in IEEE
-// fp32: scale = (max - min) / 15, bias = min, q = clamp(rint((w - bias) / scale), 0, 15); scale and
-// bias are stored rounded to the 16-bit type.  The optional outputs are fma(scale, q, bias) of the
-// stored scale and bias, rounded once.
+// Per token, head and group of G elements, in IEEE fp32: scale = (max - min) R, R the fp32 number next to
+// 1/15, bias = min, q = rint((w - bias) / scale); scale and bias are stored rounded to the 16-bit type.
+// The optional outputs are fma(scale, q, bias) of the stored scale and bias, rounded once.  The quantizer
+// of kernels_quant.cu divides by 15 instead: its stored scales are the same but where the last bit of an fp32
+// number decides a rounding to 16, its codes but where w lies halfway between two and that bit decides.
 //
 // Bound by memory: a thread owns eight elements, which are one 16-byte load, one 32-bit word of
 // codes and one 16-byte store, and a group's minimum and maximum are shuffles among its G/8 lanes,
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
             mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         }
-        const float scale = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
+        const float scale = __fmul_rn(__fsub_rn(mx, mn), 1.0f / 15.0f);
         // codes as small whole floats; the sums 2^23 + 2^22 + q round to nearest, ties to even
         constexpr float MAGIC = 12582912.0f;
         float q[8];

@@ -301,9 +301,10 @@ aq_status aq_qmm_t_residual(const aq_view* x, const aq_view* wq, const aq_view* 
  */
 
 /*
- * aq_kv_append -- quantize the keys and values of T new tokens into their slots, exactly as
- *   aq_quantize does (scale = (max - min) / 15, bias = min, ties to even, in fp32; scale and bias
- *   then rounded), both in one launch.
+ * aq_kv_append -- quantize the keys and values of T new tokens into their slots, both in one
+ *   launch, in fp32: scale = (max - min) * R, R the fp32 number next to 1/15, bias = min, q =
+ *   (x - bias) / scale to the nearest, ties to even; scale and bias then rounded.  (aq_quantize
+ *   divides by 15: a value halfway between two codes may go the other way there.)
  * k, v: [T, H, D] AQ_BF16 or AQ_F16, any strides of tokens and heads (slices of one projection's
  *   output); D a multiple of group.  Finite values, as for aq_quantize.
  * slots: DEVICE pointer to T int64 flat slots.  A negative slot is not stored (padding).  A slot

@@ -23,12 +23,26 @@ BF, F16 = torch.bfloat16, torch.float16
 # ---------------------------------------------------------------------------
 
 def _expect(x, group):
-    """The oracle's (words, scales, biases) of x [T, H, D], bit patterns as torch tensors."""
+    """(words, scales, biases) of x [T, H, D]: the formula step by step in fp32.  Against the oracle's quantizer, whose
+    scale is (max - min) / 15, stored scales and biases are within a step of their type and codes within one, the latter
+    only where the value lies halfway between two codes."""
     T, H, D = x.shape
+    f = x.float().numpy().reshape(T, H, D // group, group)
+    lo, hi = f.min(-1, keepdims=True), f.max(-1, keepdims=True)
+    s = (hi - lo) * (np.float32(1) / np.float32(15))
+    q = np.rint(np.divide(f - lo, s, out=np.zeros_like(f), where=s != 0)).astype(np.int64)
+    assert q.max() <= 15
+    words = (q.reshape(T, H, D // 8, 8) << (4 * np.arange(8))).sum(-1).astype(np.uint32).view(np.int32)
+    out = (torch.from_numpy(words), torch.from_numpy(s[..., 0]).to(x.dtype), torch.from_numpy(lo[..., 0]).to(x.dtype))
     Q = oracle.quantize(x.reshape(T * H, D).float().numpy(), group, 4, ref.dname(x.dtype))
-    return (torch.from_numpy(Q.packed.view(np.int32).copy()).view(T, H, -1),
-            torch.from_numpy(Q.scale_bits.view(np.int16).copy()).view(x.dtype).view(T, H, -1),
-            torch.from_numpy(Q.bias_bits.view(np.int16).copy()).view(x.dtype).view(T, H, -1))
+    os_, ob = (torch.from_numpy(b.view(np.int16).copy()).view(x.dtype).view(T, H, -1) for b in (Q.scale_bits, Q.bias_bits))
+    assert torch.equal(ob, out[2])
+    assert (os_.view(torch.int16).int() - out[1].view(torch.int16).int()).abs().max() <= 1
+    oq = ref.codes(torch.from_numpy(Q.packed.view(np.int32).copy()).view(T, H, -1)).numpy().reshape(q.shape)
+    off = np.nonzero(oq != q)
+    exact = ((f - lo).astype(np.float64) * 15 / np.where(s != 0, hi - lo, 1).astype(np.float64))[off]
+    assert np.all(np.abs(oq - q)[off] == 1) and np.all(np.abs(exact - np.floor(exact) - 0.5) < 1e-6)
+    return out
 
 
 def _blank(P, H, S, D, group, dtype, layout="phs"):
@@ -65,7 +79,7 @@ def _check_append(k, v, slots, kc, vc, group, outs=(None, None)):
 @pytest.mark.parametrize("T,H,D,group,S,dtype", [
     (1, 1, 64, 32, 1, BF), (1, 8, 128, 64, 16, F16), (33, 3, 96, 32, 7, BF), (32, 8, 128, 64, 64, BF),
     (257, 2, 256, 128, 48, F16), (1000, 5, 128, 128, 32, BF), (5, 1, 64, 64, 8, F16)])
-def test_append_matches_the_quantizer(T, H, D, group, S, dtype):
+def test_append_matches_the_formula(T, H, D, group, S, dtype):
     P = -(-T // S) + 2
     kv = inputs.normal((T, 2, H, D), 1.0, dtype, seed=T + D).to(DEV)
     k, v = kv[:, 0], kv[:, 1]

@@ -29,6 +29,14 @@
 //    lie anywhere in its 16-bit type's range, so p s is scaled by a power of two per group that
 //    follows the largest |s| seen (the same vote), which keeps p s below 2^15 and exact to 11 bits
 //    down to 2^-29 of that.
+//  - f16 outputs (EXACT): codes count from their middle, sum_j (p_j s) (code - 7.5) + sum_j p_j (b + 7.5 s), by
+//    MMAs whose codes are all -8 or -7 (a sign bit makes the subnormal negative; half of the tokens each), and
+//    what the rounding of p s leaves over is a second operand.  Without, the two sums cancel, over a long
+//    context all but 1/600 of them, and what the tensor cores cut off an accumulator at every step, always
+//    toward zero, and the rounding of p s come to several times the rounding of an f16 output.  131071 tokens, 32
+//    heads on 8 of 128, group 128: 9.7e-4 off, where the output's rounding is 2.1e-4, in 54 us; codes less 8
+//    in one part 4.1e-4, in two 3.2e-4; less 7.5 in two 2.2e-4, in 58 us.  For outputs of 8 bits the plain form is
+//    enough (1.9e-3 where the rounding is 1.6e-3).
 //
 //  - A warp's tile is 32 tokens where registers allow it (up to 8 query rows, head size up to 128),
 //    two pieces of 16 whose votes, waits and loop control are shared; else 16.
@@ -44,6 +52,7 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "kv_cache.h"
@@ -66,6 +75,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += codes times weights; EXACT: codes less 8 (tokens 0 to 7) or 7 (8 to 15) times weights in two parts.  HI_R, HI_R8: rows
+// r, r + 8 are low nibbles (weight 2^-24) or high ones (2^-20).
+template <bool EXACT, bool HI_R, bool HI_R8, int N>
+__device__ __forceinline__ void weigh(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[N]) {
+    constexpr uint32_t C8[2] = {0x80088008u, 0x80808080u}, C7[2] = {0x80078007u, 0x80708070u};
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        if constexpr (EXACT) mma_f16(d, C8[HI_R], C8[HI_R8], C7[HI_R], C7[HI_R8], b[i], b[i + 1]);
+        mma_f16(d, a0, a1, a2, a3, b[i], b[i + 1]);
+    }
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 block of 16-bit values across the warp
     uint32_t r;
@@ -246,6 +266,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int KS = G < 64 ? G : 64;        // dims per sub-block
     constexpr int SUBS = D / KS;
     constexpr int MT = D / 16;                 // m tiles of the output
+    constexpr bool EXACT = std::is_same<XT, f16_t>::value;     // codes count from 8, p s in two parts
     constexpr bool QREG = NT == 1 && D <= 128; // q fragments in registers
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -613,7 +634,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                     for (int g = 0; g < KG; ++g) {
                         sv[pc][g][h] = x.f(g);
-                        bv[pc][g][h] = y.f(g);
+                        bv[pc][g][h] = EXACT ? fmaf(h == 0 ? 8.0f : 7.0f, sv[pc][g][h], y.f(g)) : y.f(g);
                     }
                 }
             }
@@ -710,7 +731,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int pc = 0; pc < PCS; ++pc) {
                 // ---- p, its sums, and p s as f16 with tokens along k ----
-                uint32_t pb[KG][NT][2];
+                uint32_t pb[KG][NT][EXACT ? 4 : 2];   // EXACT: elements 2, 3 are what the rounding left over
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
@@ -736,6 +757,13 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                         const __half2 y = __floats2half2_rn(t[2], t[3]);
                         pb[g][n][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
                         pb[g][n][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                        if constexpr (EXACT) {
+                            const float2 fx = __half22float2(x), fy = __half22float2(y);
+                            const __half2 u = __floats2half2_rn(t[0] - fx.x, t[1] - fx.y);
+                            const __half2 v = __floats2half2_rn(t[2] - fy.x, t[3] - fy.y);
+                            pb[g][n][2] = transpose8(*reinterpret_cast<const uint32_t*>(&u));
+                            pb[g][n][3] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+                        }
                     }
                 }
                 // ---- O^T += V^T (p s)^T ----
@@ -754,8 +782,8 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                         for (int j = 0; j < 2; ++j) {   // nibbles 2j, 2j + 1 (rows r) and 2j + 4, 2j + 5 (rows r + 8)
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma_f16(acc[sb * 4 + 2 * j][n], nib_lo(xl), nib_lo(xh), nib_lo(yl), nib_lo(yh), pb[g][n][0], pb[g][n][1]);
-                                mma_f16(acc[sb * 4 + 2 * j + 1][n], nib_hi(xl), nib_hi(xh), nib_hi(yl), nib_hi(yh), pb[g][n][0], pb[g][n][1]);
+                                weigh<EXACT, false, false>(acc[sb * 4 + 2 * j][n], nib_lo(xl), nib_lo(xh), nib_lo(yl), nib_lo(yh), pb[g][n]);
+                                weigh<EXACT, true, true>(acc[sb * 4 + 2 * j + 1][n], nib_hi(xl), nib_hi(xh), nib_hi(yl), nib_hi(yh), pb[g][n]);
                             }
                             xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8;
                         }
@@ -766,7 +794,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                         for (int j = 0; j < 2; ++j) {   // nibble 2j (rows r) and 2j + 1 (rows r + 8) of this lane's half word
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma_f16(acc[sb * 2 + j][n], nib_lo(x), nib_hi(x), nib_lo(y), nib_hi(y), pb[g][n][0], pb[g][n][1]);
+                                weigh<EXACT, false, true>(acc[sb * 2 + j][n], nib_lo(x), nib_hi(x), nib_lo(y), nib_hi(y), pb[g][n]);
                             x >>= 8; y >>= 8;
                         }
                     }

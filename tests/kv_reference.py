@@ -52,7 +52,8 @@ def attention(q, kc, vc, pages, lengths, group, scale, window=0):
     """(out, bound): the formula in float64, and how far a result may be from it element by element.
 
     bound = u |out| + (2^-11 + 2 delta) A: the output's rounding u (half a step of its type); the rounding of a probability
-    times a scale to 11 bits (2^-11 of every term); and delta, the error of a score in fp32.  A = sum_j p_j (|s| code + |b|).
+    times a scale to 11 bits (2^-11 of every term); and delta, the error of a score in fp32.  A = sum_j p_j (|s| code + |b|),
+    for f16, where codes count from 7 or 8 (|code - 8| <= max(code, 8)), sum_j p_j (|s| max(code, 8) + |b|).
     delta = 2^-20 scale max_j sum_d |q_d| (1040 |s_jd| + |b_jd|): the codes carry an offset of at most 1024 through fp32 sums
     of 16 products per step, at most 8 steps a group, each off by at most 2^-23 of the magnitudes summed.  exp, the sums of p
     and the joins of partial sums are within a few 2^-22, which 2^-20 of the same magnitudes covers (a 2^-16 floor below)."""
@@ -73,6 +74,7 @@ def attention(q, kc, vc, pages, lengths, group, scale, window=0):
         for h in range(H):
             ks, kb = parts(tuple(x[pg, h, sl] for x in kc), group)
             vs, vb = parts(tuple(x[pg, h, sl] for x in vc), group)
+            va = torch.maximum(vs.abs(), 8 * vc[1][pg, h, sl].double().abs()[:, at]) if q.dtype == torch.float16 else vs.abs()
             mag = 1040 * kc[1][pg, h, sl].double().abs()[:, at] + kb.abs()
             for i in range(Tq):
                 pos = n - Tq + i
@@ -83,7 +85,7 @@ def attention(q, kc, vc, pages, lengths, group, scale, window=0):
                 x = qd[b, i, h * rep:(h + 1) * rep]
                 p = torch.softmax(x @ (ks + kb)[r].T * scale, -1)
                 o = p @ (vs + vb)[r]
-                A = p @ (vs.abs() + vb.abs())[r]
+                A = p @ (va + vb.abs())[r]
                 delta = 2.0 ** -20 * abs(scale) * (x.abs() @ mag[r].T).amax(-1, keepdim=True) + 2.0 ** -16
                 out[b, i, h * rep:(h + 1) * rep] = o
                 bound[b, i, h * rep:(h + 1) * rep] = u * o.abs() + (2.0 ** -11 + 2 * delta) * A

@@ -40,7 +40,8 @@ struct Args {
     uint16_t* xh;               // [T, x_pitch(K)] f16: x scaled by a power of two per token, permuted like the codes
     float* xfac;                // [T]: what takes the sums back (and the RMS norm)
     // ... and by the gate/up kernel
-    uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted
+    uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted;
+                                // where x is f16, what their rounding left over in T * topk rows more
     float* hscale;              // [T * topk, N / 16]: those powers of two
     unsigned* hmax;             // [T * topk]: the largest of each row's, as the bits of a float (zeroed by the first kernel)
     void* y;
@@ -71,7 +72,7 @@ struct Layout {
         xh = hmax + up(p * 4);
         xfac = xh + up((size_t)T * x_pitch((int)K) * 2);
         h = xfac + up((size_t)T * 4);
-        hscale = h + up(p * N * 2);
+        hscale = h + up(2 * p * N * 2);
         bytes = hscale + up(p * (N / 16) * 4);
     }
 };

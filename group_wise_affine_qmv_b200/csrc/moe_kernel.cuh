@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "moe.h"
 #include "warp_mma_kernel.cuh"
@@ -382,6 +383,12 @@ __device__ __forceinline__ void mma_step(float (&d0)[4], float (&d1)[4], float (
     }
 }
 
+// f16 numbers that an activation goes to the down product in: one for bf16 outputs, whose rounding is 8 times its
+// own; two (22 bits) for f16 outputs, whose rounding it would equal (2 tokens, 16 experts: 3.1e-4 off instead of
+// the 2.0e-4 of the output's rounding alone).
+template <typename XT>
+constexpr int PARTS = std::is_same<XT, f16_t>::value ? 2 : 1;
+
 // The power of two 2^(e - 14) with 2^e above v, in f16's range around v.
 __device__ __forceinline__ float scale_for(float v) {
     const int ex = min(max((int)((__float_as_uint(v) >> 23) & 255) - 126, -100), 127);
@@ -669,8 +676,15 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                 const float sc = scale_for(m), inv = pow2_inverse(sc);
                 if (live) {
                     uint16_t* hp = a.h + (int64_t)p * a.N + n0;
-                    hp[code_pos<BITS>(r)] = float_to_half_bits(v0 * inv * code_scale<BITS>(r), f16_t{});
-                    hp[code_pos<BITS>(r + 8)] = float_to_half_bits(v1 * inv * code_scale<BITS>(r + 8), f16_t{});
+                    const float u0 = v0 * inv * code_scale<BITS>(r), u1 = v1 * inv * code_scale<BITS>(r + 8);
+                    const uint16_t h0 = float_to_half_bits(u0, f16_t{}), h1 = float_to_half_bits(u1, f16_t{});
+                    hp[code_pos<BITS>(r)] = h0;
+                    hp[code_pos<BITS>(r + 8)] = h1;
+                    if constexpr (PARTS<XT> == 2) {
+                        hp += (int64_t)a.T * a.topk * a.N;
+                        hp[code_pos<BITS>(r)] = float_to_half_bits(u0 - half_bits_to_float(h0, f16_t{}), f16_t{});
+                        hp[code_pos<BITS>(r + 8)] = float_to_half_bits(u1 - half_bits_to_float(h1, f16_t{}), f16_t{});
+                    }
                     if (r == 0) {
                         a.hscale[(int64_t)p * nb_all + nb] = sc;
                         atomicMax(a.hmax + p, __float_as_uint(sc));
@@ -688,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
 template <int BITS, typename XT, int G, bool BLK>
 __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
-    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
+    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32, P = PARTS<XT>;
     constexpr int NST = Gm::NST_DOWN, HALF = Gm::half(BLK), STAGE = 2 * HALF, SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sb_full[2];
@@ -792,6 +806,7 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
     ptx::pdl_wait();             // the activations
     ptx::pdl_launch_dependents();
 
+    const int64_t rest = (int64_t)a.T * a.topk * a.N;    // from the activations to their rest
     int slot = 0, turn = 0, s0 = warp;   // s0: this warp's next stage, in the current entry
     float* yw = yt + warp * a.T * RP;
     for (int ent = rank; ent < entries; ent += cs, ++turn) {
@@ -832,8 +847,8 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
             constexpr int NT = decltype(tiles)::value;
             // activations and their powers of two: one tile's are fetched half a stage ahead (PRE), two tiles' for the
             // whole half at once or, where registers are short, sub-block by sub-block
-            constexpr bool AHEAD = NT * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
-            uint4 hv[NT][AHEAD ? Gm::SUBS * XV : XV];
+            constexpr bool AHEAD = NT * P * Gm::SUBS * XV <= 4, PRE = NT == 1 && AHEAD;
+            uint4 hv[NT][P][AHEAD ? Gm::SUBS * XV : XV];
             float hs[NT][AHEAD ? Gm::SUBS : 1];
             auto load_h = [&](int st, int sb, int at) {
                 const int k0 = st * Gm::SC + sb * Gm::KS;
@@ -841,8 +856,10 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int v = 0; v < XV; ++v)
-                        hv[t][at * XV + v] = reinterpret_cast<const uint4*>(hp[t] + k0)[v];
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int v = 0; v < XV; ++v)
+                            hv[t][p][at * XV + v] = reinterpret_cast<const uint4*>(hp[t] + p * rest + k0)[v];
                     hs[t][at] = hsp[t][k0 / 16];
                 }
             };
@@ -862,13 +879,15 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
                 if (hf == 1 && st * Gm::SC >= a.N) break;
                 const int g0 = st * Gm::SC / G;
                 if (AHEAD && !PRE) load_half(st);
-                uint4 hc[NT][AHEAD ? Gm::SUBS * XV : XV];
+                uint4 hc[NT][P][AHEAD ? Gm::SUBS * XV : XV];
                 float hsc[NT][AHEAD ? Gm::SUBS : 1];
                 if constexpr (AHEAD) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                        for (int v = 0; v < Gm::SUBS * XV; ++v) hc[t][v] = hv[t][v];
+                        for (int p = 0; p < P; ++p)
+#pragma unroll
+                            for (int v = 0; v < Gm::SUBS * XV; ++v) hc[t][p][v] = hv[t][p][v];
 #pragma unroll
                         for (int v = 0; v < Gm::SUBS; ++v) hsc[t][v] = hs[t][v];
                     }
@@ -896,7 +915,9 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                            for (int v = 0; v < XV; ++v) hc[t][v] = hv[t][v];
+                            for (int p = 0; p < P; ++p)
+#pragma unroll
+                                for (int v = 0; v < XV; ++v) hc[t][p][v] = hv[t][p][v];
                             hsc[t][0] = hs[t][0];
                         }
                     }
@@ -912,14 +933,18 @@ __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant_
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const __half2 f = __float2half2_rn(hsc[t][AHEAD ? sb : 0] * hinv[t]);
-                        uint32_t* hw = reinterpret_cast<uint32_t*>(&hc[t][AHEAD ? sb * XV : 0]);
 #pragma unroll
-                        for (int k = 0; k < 4 * XV; ++k) {
-                            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hw[k]), f);
-                            hw[k] = *reinterpret_cast<const uint32_t*>(&v);
+                        for (int p = 0; p < P; ++p) {
+                            uint32_t* hw = reinterpret_cast<uint32_t*>(&hc[t][p][AHEAD ? sb * XV : 0]);
+#pragma unroll
+                            for (int k = 0; k < 4 * XV; ++k) {
+                                const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hw[k]), f);
+                                hw[k] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+#pragma unroll
+                            for (int k = 0; k < Gm::STEPS; ++k)
+                                mma_step<BITS>(d[0][t], d[1][t], X[t], fr, k, hw, p == 0 && sb % Gm::SPF == 0 && k == 0);
                         }
-#pragma unroll
-                        for (int k = 0; k < Gm::STEPS; ++k) mma_step<BITS>(d[0][t], d[1][t], X[t], fr, k, hw, sb % Gm::SPF == 0 && k == 0);
                     }
                     if (sb % Gm::SPF == Gm::SPF - 1) {
                         const int f = sb / Gm::SPF;

@@ -136,7 +136,8 @@ def view(t: torch.Tensor) -> AqView:
     return v
 
 
-_PACK = {r: struct.Struct(f"<Qii{r}q{8 * (4 - r)}x{r}q{8 * (4 - r)}x") for r in (1, 2, 3, 4)}   # an AqView of rank r
+_ONE = {r: f"Qii{r}q{8 * (4 - r)}x{r}q{8 * (4 - r)}x" for r in (1, 2, 3, 4)}   # an AqView of rank r
+_PACK = {}                                                                     # ranks of a call's views -> their Struct
 _VIEW_BYTES = ctypes.sizeof(AqView)
 _scratch = threading.local()
 
@@ -148,7 +149,7 @@ def _views(*tensors) -> list:
     if buf is None:
         buf = _scratch.buf = ctypes.create_string_buffer(16 * _VIEW_BYTES)
         _scratch.base = ctypes.addressof(buf)
-    at, out = 0, []
+    at, out, ranks, fields = _scratch.base, [], [], []
     for t in tensors:
         if t is None:
             out.append(None)
@@ -160,9 +161,17 @@ def _views(*tensors) -> list:
         dt = _DT.get(t.dtype)
         if dt is None:
             raise TypeError(f"unsupported dtype {t.dtype}")
-        _PACK[rank].pack_into(buf, at, t.data_ptr(), dt, rank, *shape, *t.stride())
-        out.append(_scratch.base + at)
+        fields += (t.data_ptr(), dt, rank)
+        fields += shape
+        fields += t.stride()
+        ranks.append(rank)
+        out.append(at)
         at += _VIEW_BYTES
+    ranks = tuple(ranks)
+    pack = _PACK.get(ranks)
+    if pack is None:
+        pack = _PACK[ranks] = struct.Struct("<" + "".join(_ONE[r] for r in ranks))
+    pack.pack_into(buf, 0, *fields)
     return out
 
 
@@ -375,7 +384,7 @@ def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, 
     if pages.shape[0] != q.shape[0] or lengths.shape[0] != q.shape[0]:
         raise ValueError("pages and lengths need one entry per sequence")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if scale is None:
         scale = q.shape[-1] ** -0.5
     max_pages = pages.shape[1]
@@ -383,7 +392,7 @@ def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, 
         vq, vk, *rest, vo = _views(q, *k_cache, *v_cache, out)
         need = ctypes.c_size_t()
         _check(lib, lib.aq_kv_attention_workspace(vq, vk, max_pages, ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=q.device) if need.value else None
+        ws = q.new_empty(need.value, dtype=torch.uint8) if need.value else None
         _check(lib, lib.aq_kv_attention(vq, vk, *rest, group, bits, pages.data_ptr(), pages.stride(0), max_pages,
                                         lengths.data_ptr(), scale, window, vo, ws.data_ptr() if need.value else None,
                                         need.value, stream))
@@ -397,11 +406,11 @@ def aq_moe_swiglu(x, logits, top_k: int, gate, up, down, group: int, bits: int, 
     rms_eps > 0: x RMS-normalised per token first.  out may be residual or x itself."""
     lib = load_library()
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype or x.dtype, memory_format=torch.contiguous_format)
     with _On(x) as stream:
         need = ctypes.c_size_t()
         _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, x.shape[1], gate[0].shape[-2], ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        ws = x.new_empty(need.value, dtype=torch.uint8)
         vx, vl, *banks, vr, vy = _views(x, logits, *gate, *up, *down, residual, out)
         _check(lib, lib.aq_moe_swiglu(vx, vl, top_k, 1 if norm_topk else 0, *banks, group, bits, rms_eps, vr, vy,
                                       ws.data_ptr(), need.value, stream))

@@ -1047,7 +1047,8 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     const bool blk_down = a.down.blk && kgd <= DOWN_GROUPS;
     const size_t smem_down = Gm::ring(Gm::NST_DOWN, blk_down) + (blk_down ? (size_t)2 * 128 * kgd : 0) + WARPS * a.T * RP * sizeof(float);
     // The down kernel's CTAs all at once on the device, one cluster of up to eight per 32 columns of y, no more
-    // CTAs in it than there can be entries (32 tokens, 128 experts: 352 CTAs where 296 fit took 600 us, 264 450 us).
+    // CTAs in it than there can be entries (64 tokens, 64 experts of 4 bits: 384 CTAs
+    // of 444 that fit 116 us the layer, 512 CTAs 134).
     const int blocks = (a.K + ROWS - 1) / ROWS;
     const int fit = 148 * (int)std::min<size_t>(3, 227 * 1024 / (smem_down + 1024));
     a.cs = std::max(1, std::min({8, fit / blocks, a.T * a.topk, a.E}));
@@ -1085,22 +1086,20 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     cfg.blockDim = dim3(32 * PREP_WARPS);
     e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT>, a);
     if (e != cudaSuccess) return e;
-    // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM).  With up
-    // to two items for every CTA that fits, four warps share an item: its latency counts, not the throughput (two
-    // tokens, 16 experts of 4 bits: 12.4 against 15.3 us; one token, 128 experts of 8 bits, over twice as many
-    // items: 58 against 54 us).  The same kernel takes rows whose scales do not fit a warp's block.
+    // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM).  With no
+    // more items than CTAs that fit, four warps share an item: its latency counts, not the throughput (128 items, 16
+    // experts of 4 bits: 13.6 against 16.4 us the layer; 512 items, 128 experts of 4 bits: 30.5 against 29.0; 1408 items,
+    // of 8 bits: 48 against 41).  The same kernel takes rows whose scales do not fit a warp's block.
     const int64_t pairs = (int64_t)a.T * a.topk;
     const int64_t most = pairs < a.E + pairs / TB ? pairs : a.E + pairs / TB;
     const int64_t items = most * (a.N / 16), all = 148 * 3;
-    bool full = items >= all;
     cfg.blockDim = dim3(THREADS);
-    if (items <= 2 * all || kg > UP_GROUPS || !a.gate.blk || !a.up.blk) {
+    if (items <= all || kg > UP_GROUPS || !a.gate.blk || !a.up.blk) {
         cfg.gridDim = dim3((unsigned)(items < all ? items : all));
         cfg.dynamicSmemBytes = smem_shared;
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, true>, a);
     } else {
         const int64_t ctas = (items + WARPS - 1) / WARPS;
-        full = ctas >= all;
         cfg.gridDim = dim3((unsigned)(ctas < all ? ctas : all));
         cfg.dynamicSmemBytes = smem_own;
         e = cudaLaunchKernelEx(&cfg, gate_up_kernel<BITS, XT, G, false>, a);
@@ -1109,12 +1108,6 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)((a.K + ROWS - 1) / ROWS * a.cs));
     cfg.dynamicSmemBytes = smem_down;
     cfg.numAttrs = a.cs > 1 ? 2 : 1;
-    // Early only next to a gate/up grid that leaves room: clusters that squeeze in between its last CTAs end up
-    // placed so that others have to wait for them (32 tokens, 128 experts: 680 us against 473).
-    if (full) {
-        cfg.attrs = attr + 1;
-        cfg.numAttrs -= 1;
-    }
     return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true>, a)
                     : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false>, a);
 }

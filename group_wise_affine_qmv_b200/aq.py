@@ -150,6 +150,7 @@ def _views(*tensors) -> list:
         buf = _scratch.buf = ctypes.create_string_buffer(16 * _VIEW_BYTES)
         _scratch.base = ctypes.addressof(buf)
     at, out, ranks, fields = _scratch.base, [], [], []
+    dev = tensors[0].get_device()
     for t in tensors:
         if t is None:
             out.append(None)
@@ -161,6 +162,8 @@ def _views(*tensors) -> list:
         dt = _DT.get(t.dtype)
         if dt is None:
             raise TypeError(f"unsupported dtype {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
         fields += (t.data_ptr(), dt, rank)
         fields += shape
         fields += t.stride()

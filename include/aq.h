@@ -340,7 +340,7 @@ aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots,
  * workspace: DEVICE memory of at least the bytes aq_kv_attention_workspace gives for the same q,
  *   k_wq and max_pages, 16-byte aligned, used by this call only while it runs on its stream.
  * Scores, softmax statistics and sums are fp32; the query is exact, the product of a
- * probability and a value's scale is rounded to 11 bits.  Meant for decode and short runs of new
+ * probability and a value's scale is carried in 11 bits for AQ_BF16 and in 22 for AQ_F16.  Meant for decode and short runs of new
  * tokens: the cache is read once per 32 query rows (D 256: 16) of a key/value head.
  */
 aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases,
@@ -369,8 +369,9 @@ aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64
  * and makes its token's y NaN.
  * Every expert that some token chose is read once per 16 of its tokens; both contractions are exact
  * in W with fp32 sums; x enters exactly, and the weighted activations pass between the launches
- * with 11 bits of mantissa (relative to the largest of 16).  The same call gives the same bits; the order of a token's sum over its experts may
- * depend on which experts the other tokens chose.
+ * with 11 bits of mantissa for AQ_BF16 x and 22 for AQ_F16 (relative to the largest of 16).  The
+ * same call gives the same bits; the order of a token's sum over its experts may depend on which
+ * experts the other tokens chose.
  * workspace: DEVICE memory of at least the bytes aq_moe_swiglu_workspace(T, top_k, K, N) gives,
  *   16-byte aligned, used by this call only while it runs on its stream.
  */

@@ -414,6 +414,16 @@ def test_attention_captured_replayed_and_on_two_streams():
     aq.aq_device_error()
 
 
+def test_tensors_of_another_device_are_refused():
+    q, kc, vc, pages, n = _case(1, 2, 1, 64, 64, 16, 1, [20], BF)
+    dk, dv = ref.to_dev(kc), ref.to_dev(vc)
+    with pytest.raises(ValueError):
+        aq.aq_kv_attention(q.to(DEV), (dk[0], dk[1].cpu(), dk[2]), dv, pages.to(DEV), n.to(DEV), 64, 4)
+    with pytest.raises(ValueError):
+        aq.aq_kv_append(q[0].to(DEV), q[0], n.to(DEV), dk, dv, 64, 4)
+    aq.aq_device_error()
+
+
 def test_append_then_attention_token_by_token():
     """A prompt and then single tokens: the cache as appended gives what the whole sequence's own keys and values give."""
     B, Hq, H, D, group, S, n0, steps = 2, 4, 2, 128, 64, 16, 30, 6

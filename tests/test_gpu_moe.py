@@ -268,3 +268,15 @@ def test_no_tokens():
     banks, x, logits = setup(1, 4, 128, 64, 64, 4, BF)
     y = call(banks, x[:0], logits[:0], 2, 64, 4)
     assert y.shape == (0, 128)
+
+
+def test_tensors_of_another_device_are_refused():
+    banks, x, logits = setup(2, 4, 128, 64, 64, 4, BF)
+    dev = [b.dev for b in banks]
+    for i in range(3):
+        mixed = list(dev)
+        mixed[i] = (dev[i][0], dev[i][1].cpu(), dev[i][2])
+        with pytest.raises(ValueError):
+            aq.aq_moe_swiglu(x.to(DEV), logits.to(DEV), 2, *mixed, 64, 4)
+    with pytest.raises(ValueError):
+        aq.aq_moe_swiglu(x.to(DEV), logits, 2, *dev, 64, 4)

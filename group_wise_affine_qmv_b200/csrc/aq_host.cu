@@ -545,6 +545,7 @@ aq_status check_attention_q(const aq_view* q, const aq_view* k_wq, int64_t max_p
     if (D != 64 && D != 128 && D != 256) return fail(AQ_ERR_UNSUPPORTED, "head size %lld (64, 128 and 256 are supported)", (long long)D);
     if (H < 1 || Hq % H != 0) return fail(AQ_ERR_SHAPE, "%lld query heads are not a multiple of %lld key/value heads", (long long)Hq, (long long)H);
     if (max_pages < 0) return fail(AQ_ERR_SHAPE, "max_pages < 0");
+    if (k_wq->shape[0] > 0x7fffffff) return fail(AQ_ERR_UNSUPPORTED, "more than 2^31 pages");
     if (max_pages > (1 << 30) || S > (1 << 30) || max_pages * S > (1 << 30))
         return fail(AQ_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
     // work units of 64 tokens, heads and 8 query rows, counted in 32 bits by the kernel
@@ -1244,6 +1245,13 @@ AQ_API aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq
     a.v_page = (uint32_t)(a.v.w_page * 4);
     a.v_slot = (uint32_t)(a.v.w_slot * 4);
     a.fast = fast ? 1 : 0;
+    a.scp = kg > 1 ? 1 : 0;
+    for (const aq::kv::Side* d : {&a.k, &a.v}) {
+        const uintptr_t at = (uintptr_t)d->scales | (uintptr_t)d->biases;
+        if (at % (2 * kg) != 0) a.scp = 0;
+        for (int64_t x : {d->s_page, d->s_head, d->s_slot, d->b_page, d->b_head, d->b_slot})
+            if (x % kg != 0) a.scp = 0;
+    }
     const int unit = aq::kv::unit_tokens((int)D, s.nt);
     a.unit_slots = S > 0 ? (int)(unit % S) : 0;
     a.split = s.split;

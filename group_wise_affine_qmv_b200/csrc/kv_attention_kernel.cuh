@@ -105,6 +105,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int size) { 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 template <int N>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, bool on) {   // 4, 8 or 16 bytes, or as many zeros
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N < 4 ? 4 : N), "r"(on ? N : 0) : "memory");
+}
+template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ float2 half_pair(uint32_t v, bf16_t) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -270,7 +274,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int KS = G < 64 ? G : 64;        // dims per sub-block
     constexpr int SUBS = D / KS;
     constexpr int MT = D / 16;                 // m tiles of the output
-    constexpr bool EXACT = std::is_same<XT, f16_t>::value;     // codes count from 8, p s in two parts
+    constexpr bool EXACT = std::is_same<XT, f16_t>::value;     // codes count from 7.5, p s in two parts
     constexpr bool QREG = NT == 1 && D <= 128; // q fragments in registers
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -408,50 +412,87 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
             l_slot += a.unit_slots;
             if (l_slot >= a.S) l_slot -= a.S;
         };
-        // any page size and strides: rows one by one, scales through registers
-        auto load_any = [&](int t00, int st) {
-#pragma unroll 1
-            for (int pc = 0; pc < PCS; ++pc) {
-                const int t0 = t00 + pc * TILE;
-                const uint32_t dst = ring_s + st * Gm::STAGE + pc * Gm::PIECE;
-                for (int x = lane; x < TILE * Gm::CH; x += 32) {
-                    const int row = x / Gm::CH, ch = x % Gm::CH;
-                    const int t = t0 + row;
-                    if (t >= sp.len) continue;
-                    const int pg = t / a.S, sl = t - pg * a.S;
-                    int64_t pid = __ldcg(pages + pg);
-                    const bool ok = (uint64_t)pid < (uint64_t)a.P;
-                    missing |= !ok;
-                    if (!ok) pid = 0;
-                    const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.k.wq + pid * a.k.w_page + head * a.k.w_head + sl * a.k.w_slot);
-                    const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.v.wq + pid * a.v.w_page + head * a.v.w_head + sl * a.v.w_slot);
-                    cp16(dst + ch * Gm::CP + row * 16, kp + ch * 16, ok ? 16 : 0);
-                    cp16(dst + Gm::CODES + ch * Gm::CP + Gm::vpos(row) * 16, vp + ch * 16, ok ? 16 : 0);
-                }
-                uint16_t* sc = reinterpret_cast<uint16_t*>(ring + st * Gm::STAGE + pc * Gm::PIECE + 2 * Gm::CODES);
-                for (int x = lane; x < TILE * KG; x += 32) {
-                    const int row = x / KG, g = x % KG;
-                    const int t = t0 + row;
-                    uint16_t v4[4] = {0, 0, 0, 0};
-                    if (t < sp.len) {
-                        const int pg = t / a.S, sl = t - pg * a.S;
-                        const int64_t pid = __ldcg(pages + pg);
-                        if ((uint64_t)pid < (uint64_t)a.P) {
-                            v4[0] = __ldcg(a.k.scales + pid * a.k.s_page + head * a.k.s_head + sl * a.k.s_slot + g);
-                            v4[1] = __ldcg(a.k.biases + pid * a.k.b_page + head * a.k.b_head + sl * a.k.b_slot + g);
-                            v4[2] = __ldcg(a.v.scales + pid * a.v.s_page + head * a.v.s_head + sl * a.v.s_slot + g);
-                            v4[3] = __ldcg(a.v.biases + pid * a.v.b_page + head * a.v.b_head + sl * a.v.b_slot + g);
-                        }
-                    }
+        // Any page size and strides: every token has a page and a slot of its own, looked up by the lanes r of
+        // its piece (lane % 16) a tile ahead.  Scales and biases copy row by row where rows of them allow it
+        // (scp); else they go through registers, which are stored with the next tile's issue.  (32 sequences of 500 to
+        // 4096 tokens, 16 heads on 8 of 128, pages of 8: 47 us against 41 in pages of 64; each lookup and scale waited
+        // for in its own tile took 108.  Pages of 1 and one group a head: 62 us.)
+        int64_t id_ahead[PCS];
+        int sl_ahead[PCS], late_st = -1;
+        uint16_t late[PCS][2][KG];
+        auto fetch_rows = [&](int i) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[k * TILE * KG + x] = v4[k];
+            for (int pc = 0; pc < PCS; ++pc) {
+                const int t = tw + i * UNIT + pc * TILE + (lane & 15);
+                id_ahead[pc] = -1;
+                sl_ahead[pc] = 0;
+                if (i < nt && t < sp.len) {
+                    const int pg = t / a.S;
+                    sl_ahead[pc] = t - pg * a.S;
+                    id_ahead[pc] = __ldcg(pages + pg);
                 }
             }
         };
+        auto store_late = [&]() {
+            if (late_st < 0) return;
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int g = 0; g < KG; ++g)
+                        reinterpret_cast<uint16_t*>(ring + late_st * Gm::STAGE + pc * Gm::PIECE + 2 * Gm::CODES)
+                            [(2 * x + (lane >> 4)) * TILE * KG + (lane & 15) * KG + g] = late[pc][x][g];
+            late_st = -1;
+        };
+        auto load_any = [&](int i, int st) {
+            uint32_t id[PCS];            // ~0: no token, or no such page
+            int sl[PCS];
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc) {
+                id[pc] = (uint64_t)id_ahead[pc] < (uint64_t)a.P ? (uint32_t)id_ahead[pc] : 0xffffffffu;
+                sl[pc] = sl_ahead[pc];
+                missing |= id[pc] == 0xffffffffu && tw + i * UNIT + pc * TILE + (lane & 15) < sp.len;
+            }
+            fetch_rows(i + 1);
+#pragma unroll
+            for (int pc = 0; pc < PCS; ++pc) {
+                const uint32_t dst = ring_s + st * Gm::STAGE + pc * Gm::PIECE;
+#pragma unroll
+                for (int x = 0; x < TILE * Gm::CH / 32; ++x) {
+                    const int row = (lane + 32 * x) / Gm::CH, ch = lane % Gm::CH;
+                    uint32_t pid = __shfl_sync(0xffffffffu, id[pc], row);
+                    const int slot = __shfl_sync(0xffffffffu, sl[pc], row);
+                    const int size = pid != 0xffffffffu ? 16 : 0;
+                    if (!size) pid = 0;
+                    cp16(dst + ch * Gm::CP + row * 16,
+                         reinterpret_cast<const uint8_t*>(a.k.wq + pid * a.k.w_page + head * a.k.w_head + slot * a.k.w_slot) + ch * 16, size);
+                    cp16(dst + Gm::CODES + ch * Gm::CP + Gm::vpos(row) * 16,
+                         reinterpret_cast<const uint8_t*>(a.v.wq + pid * a.v.w_page + head * a.v.w_head + slot * a.v.w_slot) + ch * 16, size);
+                }
+                const bool ok = id[pc] != 0xffffffffu;
+                const int64_t pid = ok ? id[pc] : 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {        // keys, values; scales by lanes 0 to 15, biases by the others
+                    const Side& sd = x ? a.v : a.k;
+                    const uint16_t* src = lane < 16 ? sd.scales + pid * sd.s_page + head * sd.s_head + sl[pc] * sd.s_slot
+                                                    : sd.biases + pid * sd.b_page + head * sd.b_head + sl[pc] * sd.b_slot;
+                    if (KG > 1 && a.scp) {
+                        cp_small<KG * 2>(dst + 2 * Gm::CODES + (2 * x + (lane >> 4)) * Gm::SB + (lane & 15) * KG * 2, src, ok);
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < KG; ++g) late[pc][x][g] = ok ? __ldcg(src + g) : (uint16_t)0;
+                    }
+                }
+            }
+            if (KG == 1 || !a.scp) late_st = st;
+        };
+        if constexpr (!FAST) fetch_rows(0);
         auto issue = [&](int i, int st) {
+            if constexpr (!FAST) store_late();
             if (i < nt) {
                 if constexpr (FAST) load_fast(i, ring_s + st * Gm::STAGE);
-                else load_any(tw + i * UNIT, st);
+                else load_any(i, st);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };

@@ -53,6 +53,7 @@ struct AttnArgs {
     int window;                 // 0: none
     float scale_log2;           // softmax scale * log2(e)
     int fast;                   // 1: 16-token tiles lie inside a page and copy as whole 16-byte pieces
+    int scp;                    // not fast: a row's scales (and biases) are one aligned copy of 4, 8 or 16 bytes
     uint32_t k_page, k_slot, v_page, v_slot;   // fast: strides of the codes in bytes
     int unit_slots;             // fast: a unit's tokens past whole pages
     int split;                  // 1: a combine launch follows (an item's units may be shared by CTAs)

@@ -227,6 +227,11 @@ def test_attention_refusals(lib, case, status):
     assert got == status if status else got in ("AQ_ERR_CUDA", "AQ_ERR_DEVICE"), (got, lib.aq_last_error_message())
 
 
+def test_attention_refuses_more_pages_than_it_counts(lib):
+    q, c = torch.zeros(2, 1, 4, 128, dtype=BF), [t[:1].expand(2 ** 31, *t.shape[1:]) for t in side()]
+    assert attention(lib, q, c, c, torch.empty_like(q)) == "AQ_ERR_UNSUPPORTED"
+
+
 def test_attention_workspace_depends_on_sizes_only(lib):
     def need(B, Tq, Hq, D, H, S, pages):
         n = ctypes.c_size_t()

@@ -219,6 +219,25 @@ def test_attention_layouts_give_the_same_bits(layout, S):
     assert torch.equal(out, base)
 
 
+@pytest.mark.parametrize("D,group", [(128, 64), (128, 32), (256, 32), (256, 64), (64, 64)])
+def test_attention_scales_past_their_boundary(D, group):
+    """Scales and biases that start one element past where a row of them could be copied whole."""
+    q, kc, vc, pages, n = _case(2, 8, 4, D, group, 16, 1, [150, 37], F16, seed=12)
+    base = _run(q, kc, vc, pages, n, group)
+
+    def past(side):
+        dev = list(ref.to_dev(side))
+        for i in (1, 2):
+            flat = torch.zeros(dev[i].numel() + 1, dtype=dev[i].dtype, device=DEV)
+            flat[1:] = dev[i].flatten()
+            dev[i] = flat[1:].view(dev[i].shape)
+        return tuple(dev)
+
+    out = aq.aq_kv_attention(q.to(DEV), past(kc), past(vc), pages.to(DEV), n.to(DEV), group, 4)
+    aq.aq_device_error()
+    assert torch.equal(out, base)
+
+
 def test_attention_strided_queries_outputs_and_table():
     q, kc, vc, pages, n = _case(2, 6, 3, 64, 32, 16, 2, [70, 19], BF, seed=4)
     base = _run(q, kc, vc, pages, n, 32)

@@ -35,7 +35,8 @@
 //    context all but 1/600 of them, and what the tensor cores cut off an accumulator at every step, always
 //    toward zero, and the rounding of p s come to several times the rounding of an f16 output.  131071 tokens, 32
 //    heads on 8 of 128, group 128: 9.7e-4 off, where the output's rounding is 2.1e-4, in 54 us; codes less 8
-//    in one part 4.1e-4, in two 3.2e-4; less 7.5 in two 2.2e-4, in 58 us.  For outputs of 8 bits the plain form is
+//    in one part 4.1e-4, in two 3.2e-4; less 7.5 in two 2.2e-4, in 58 us (with one such MMA a group, added to every
+//    accumulator before its codes: 2% faster, 4.9e-4).  For outputs of 8 bits the plain form is
 //    enough (1.9e-3 where the rounding is 1.6e-3).
 //
 //  - A warp's tile is 32 tokens where registers allow it (up to 8 query rows, head size up to 128),

@@ -433,6 +433,28 @@ def test_attention_captured_replayed_and_on_two_streams():
     aq.aq_device_error()
 
 
+@pytest.mark.parametrize("S", [64, 63])
+def test_caches_past_four_gigabytes(S):
+    """Offsets of more than 32 bits: appended to and read from the last pages of a large cache as from a small one."""
+    P, H, D, group, T = 140000, 8, 128, 64, 150
+    k, v = (inputs.normal((T, H, D), 1.0, BF, seed=s).to(DEV) for s in (40, 41))
+    q = inputs.normal((1, 1, 16, D), 1.0, BF, seed=42).to(DEV)
+    n = torch.tensor([T], device=DEV)
+    got = []
+    for pages in (P, 4):
+        kc, vc = (tuple(torch.zeros(pages, H, S, w, dtype=t, device=DEV) for w, t in ((D // 8, torch.int32), (D // group, BF), (D // group, BF)))
+                  for _ in range(2))
+        ids = torch.tensor([[pages - 1, pages - 3, pages - 2]], device=DEV)
+        t = torch.arange(T, device=DEV)
+        aq.aq_kv_append(k, v, ids[0, t // S] * S + t % S, kc, vc, group, 4)
+        got.append(aq.aq_kv_attention(q, kc, vc, ids, n, group, 4))
+        assert all(int(x[:pages - 3].count_nonzero()) == 0 for c in (kc, vc) for x in c)
+        del kc, vc
+    assert torch.equal(got[0], got[1]) and got[0].abs().max() > 0
+    aq.aq_device_error()
+    torch.cuda.empty_cache()
+
+
 def test_tensors_of_another_device_are_refused():
     q, kc, vc, pages, n = _case(1, 2, 1, 64, 64, 16, 1, [20], BF)
     dk, dv = ref.to_dev(kc), ref.to_dev(vc)

@@ -29,15 +29,21 @@
 //    lie anywhere in its 16-bit type's range, so p s is scaled by a power of two per group that
 //    follows the largest |s| seen (the same vote), which keeps p s below 2^15 and exact to 11 bits
 //    down to 2^-29 of that.
-//  - f16 outputs (EXACT): codes count from their middle, sum_j (p_j s) (code - 7.5) + sum_j p_j (b + 7.5 s), by
-//    MMAs whose codes are all -8 or -7 (a sign bit makes the subnormal negative; half of the tokens each), and
-//    what the rounding of p s leaves over is a second operand.  Without, the two sums cancel, over a long
-//    context all but 1/600 of them, and what the tensor cores cut off an accumulator at every step, always
-//    toward zero, and the rounding of p s come to several times the rounding of an f16 output.  131071 tokens, 32
-//    heads on 8 of 128, group 128: 9.7e-4 off, where the output's rounding is 2.1e-4, in 54 us; codes less 8
-//    in one part 4.1e-4, in two 3.2e-4; less 7.5 in two 2.2e-4, in 58 us (with one such MMA a group, added to every
-//    accumulator before its codes: 2% faster, 4.9e-4).  For outputs of 8 bits the plain form is
-//    enough (1.9e-3 where the rounding is 1.6e-3).
+//  - Values: the sum over a context cancels.  Codes are positive, sum (p s) code and sum p b all but 1/1000 of each
+//    other after 10^5 tokens, and the tensor cores cut an accumulator toward zero at every step, always the same
+//    way: one running through a context of 131072 tokens left 5e-2 of the result's size (bf16 rounds 1.7e-3).  So
+//      a tile's MMAs start from minus the middle of the codes (7.5, as 8 and 7 for half of the tokens each; one more MMA a
+//      group, codes all -8 or -7: a sign bit makes the subnormal negative) and their result is added to an fp32 sum,
+//      rounded to nearest; the bias term takes p (b + 7.5 s);
+//      every second piece goes in as its mirror image, 15 - code with negative weights, whose cut goes the other
+//      way (w ^ mask costs nothing in front of an AND).
+//    Centred codes in one long accumulator do for channels around zero, but where some channels of a group lie far
+//    off, the others' codes are all small: f16, one channel of 32 at 20 deviations: the others 2.6e-3 off after 8192 tokens
+//    and 9.2e-2 after 131072; as it is 2.2e-4 and 4.6e-4 (rounding: 2.1e-4).  Without the mirror 3.0e-4 and 8.6e-4.  Cost: bf16
+//    3 to 5% (32 sequences of 9001 to 32768: 252 against 243 us), f16 0 to 4%.
+//  - f16 outputs carry p s as two f16 numbers (PARTS): one rounding of 11 bits for every term would equal the output's
+//    own.  131071 tokens, 32 heads on 8 of 128, group 128: 2.06e-4 off, the output's rounding 2.05e-4; bf16 in one part
+//    1.70e-3, its rounding 1.69e-3.
 //
 //  - A warp's tile is 32 tokens where registers allow it (up to 8 query rows, head size up to 128),
 //    two pieces of 16 whose votes, waits and loop control are shared; else 16.
@@ -81,16 +87,48 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d += codes times weights; EXACT: codes less 8 (tokens 0 to 7) or 7 (8 to 15) times weights in two parts.  HI_R, HI_R8: rows
-// r, r + 8 are low nibbles (weight 2^-24) or high ones (2^-20).
-template <bool EXACT, bool HI_R, bool HI_R8, int N>
-__device__ __forceinline__ void weigh(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[N]) {
-    constexpr uint32_t C8[2] = {0x80088008u, 0x80808080u}, C7[2] = {0x80078007u, 0x80708070u};
+// d = a b + c
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// The pieces of a tile, odd ones (odd tiles where a tile is one piece) with complemented codes and negative weights: mask p.
+template <int PCS>
+struct Flip {
+    uint32_t odd;                     // PCS 1: all ones in odd tiles
+    __device__ __forceinline__ uint32_t mask(int p) const { return PCS == 1 ? odd : p & 1 ? ~0u : 0u; }
+};
+// -sum of a tile's weights times 8 (tokens 0 to 7 of a piece) or 7 (8 to 15), as the sums of low nibbles (mid[0], mid[1]) and of
+// high ones
+template <int PCS, int N>
+__device__ __forceinline__ void middle(float (&mid)[4], const uint32_t (&b)[PCS][N], Flip<PCS> f) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        if constexpr (EXACT) mma_f16(d, C8[HI_R], C8[HI_R8], C7[HI_R], C7[HI_R8], b[i], b[i + 1]);
-        mma_f16(d, a0, a1, a2, a3, b[i], b[i + 1]);
+    for (int i = 0; i < PCS * N; i += 2) {
+        const int p = i / N;
+        const uint32_t lo = f.mask(p) & 0x000F000Fu, hi = f.mask(p) & 0x00F000F0u;
+        if (i == 0) mma_from(mid, 0x80088008u ^ lo, 0x80808080u ^ hi, 0x80078007u ^ lo, 0x80708070u ^ hi, b[p][i % N], b[p][i % N + 1], 0.0f, 0.0f, 0.0f, 0.0f);
+        else mma_f16(mid, 0x80088008u ^ lo, 0x80808080u ^ hi, 0x80078007u ^ lo, 0x80708070u ^ hi, b[p][i % N], b[p][i % N + 1]);
     }
+}
+// sum += (codes - middle) weights.  HI_R, HI_R8: rows r, r + 8 are low nibbles (weight 2^-24) or high ones (2^-20).
+template <bool HI_R, bool HI_R8, int PCS, int N>
+__device__ __forceinline__ void weigh(float (&sum)[4], const uint32_t (&a)[PCS][4], const uint32_t (&b)[PCS][N], const float (&mid)[4], Flip<PCS> f) {
+    float d[4];
+#pragma unroll
+    for (int i = 0; i < PCS * N; i += 2) {
+        const int p = i / N;
+        const auto nib = [&](int k, bool hi) { return hi ? nib_hi(a[p][k] ^ f.mask(p)) : nib_lo(a[p][k] ^ f.mask(p)); };
+        if (i == 0)
+            mma_from(d, nib(0, HI_R), nib(1, HI_R8), nib(2, HI_R), nib(3, HI_R8), b[p][i % N], b[p][i % N + 1],
+                     mid[HI_R ? 2 : 0], mid[HI_R ? 3 : 1], mid[HI_R8 ? 2 : 0], mid[HI_R8 ? 3 : 1]);
+        else
+            mma_f16(d, nib(0, HI_R), nib(1, HI_R8), nib(2, HI_R), nib(3, HI_R8), b[p][i % N], b[p][i % N + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += d[e];
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 block of 16-bit values across the warp
     uint32_t r;
@@ -275,7 +313,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int KS = G < 64 ? G : 64;        // dims per sub-block
     constexpr int SUBS = D / KS;
     constexpr int MT = D / 16;                 // m tiles of the output
-    constexpr bool EXACT = std::is_same<XT, f16_t>::value;     // codes count from 7.5, p s in two parts
+    constexpr int PARTS = std::is_same<XT, f16_t>::value ? 2 : 1;   // f16 numbers that carry a p s
     constexpr bool QREG = NT == 1 && D <= 128; // q fragments in registers
 
     extern __shared__ __align__(128) uint8_t smem[];
@@ -680,7 +718,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                     for (int g = 0; g < KG; ++g) {
                         sv[pc][g][h] = x.f(g);
-                        bv[pc][g][h] = EXACT ? fmaf(h == 0 ? 8.0f : 7.0f, sv[pc][g][h], y.f(g)) : y.f(g);
+                        bv[pc][g][h] = fmaf(h == 0 ? 8.0f : 7.0f, sv[pc][g][h], y.f(g));
                     }
                 }
             }
@@ -774,10 +812,11 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                     }
                 }
             }
+            uint32_t pb[KG][NT][PCS][2 * PARTS];   // elements 2, 3: what the rounding left over
+            const Flip<PCS> flip{(i & 1) ? ~0u : 0u};
 #pragma unroll
             for (int pc = 0; pc < PCS; ++pc) {
                 // ---- p, its sums, and p s as f16 with tokens along k ----
-                uint32_t pb[KG][NT][EXACT ? 4 : 2];   // EXACT: elements 2, 3 are what the rounding left over
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
@@ -787,7 +826,8 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                     l[n][1] += p[1] + p[3];
 #pragma unroll
                     for (int g = 0; g < KG; ++g) {
-                        const float m0 = sv[pc][g][0] * vmul[g], m1 = sv[pc][g][1] * vmul[g];
+                        const float vm = flip.mask(pc) ? -vmul[g] : vmul[g];
+                        const float m0 = sv[pc][g][0] * vm, m1 = sv[pc][g][1] * vm;
                         float t[4] = {p[0] * m0, p[1] * m0, p[2] * m1, p[3] * m1};
                         if (full) {
                             ab[g][n][0] = fmaf(p[0], bv[pc][g][0], fmaf(p[2], bv[pc][g][1], ab[g][n][0]));
@@ -801,49 +841,58 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                         }
                         const __half2 x = __floats2half2_rn(t[0], t[1]);
                         const __half2 y = __floats2half2_rn(t[2], t[3]);
-                        pb[g][n][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
-                        pb[g][n][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
-                        if constexpr (EXACT) {
+                        pb[g][n][pc][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
+                        pb[g][n][pc][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+                        if constexpr (PARTS == 2) {
                             const float2 fx = __half22float2(x), fy = __half22float2(y);
                             const __half2 u = __floats2half2_rn(t[0] - fx.x, t[1] - fx.y);
                             const __half2 v = __floats2half2_rn(t[2] - fy.x, t[3] - fy.y);
-                            pb[g][n][2] = transpose8(*reinterpret_cast<const uint32_t*>(&u));
-                            pb[g][n][3] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
+                            pb[g][n][pc][2] = transpose8(*reinterpret_cast<const uint32_t*>(&u));
+                            pb[g][n][pc][3] = transpose8(*reinterpret_cast<const uint32_t*>(&v));
                         }
                     }
                 }
-                // ---- O^T += V^T (p s)^T ----
-                const uint8_t* vp = kt + pc * Gm::PIECE + Gm::CODES + v_lane;
+            }
+            // ---- O^T += V^T (p s)^T ----
+            const uint8_t* vp = kt + Gm::CODES + v_lane;
+            float mid[NT][4];
 #pragma unroll
-                for (int sb = 0; sb < SUBS; ++sb) {
-                    const int g = sb * KS / G;
+            for (int sb = 0; sb < SUBS; ++sb) {
+                const int g = sb * KS / G;
+                if (sb * KS % G == 0)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) middle(mid[n], pb[g][n], flip);
+                uint32_t a[PCS][4];
+#pragma unroll
+                for (int pc = 0; pc < PCS; ++pc) {
                     uint32_t w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)   // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-                        w[k] = *reinterpret_cast<const uint32_t*>(vp + sb * (KS / 32) * Gm::CP + k * 64);
+                        w[k] = *reinterpret_cast<const uint32_t*>(vp + pc * Gm::PIECE + sb * (KS / 32) * Gm::CP + k * 64);
                     if constexpr (KS == 64) {
-                        uint32_t xl = __byte_perm(w[0], w[1], 0x5410), xh = __byte_perm(w[0], w[1], 0x7632);
-                        uint32_t yl = __byte_perm(w[2], w[3], 0x5410), yh = __byte_perm(w[2], w[3], 0x7632);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {   // nibbles 2j, 2j + 1 (rows r) and 2j + 4, 2j + 5 (rows r + 8)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                weigh<EXACT, false, false>(acc[sb * 4 + 2 * j][n], nib_lo(xl), nib_lo(xh), nib_lo(yl), nib_lo(yh), pb[g][n]);
-                                weigh<EXACT, true, true>(acc[sb * 4 + 2 * j + 1][n], nib_hi(xl), nib_hi(xh), nib_hi(yl), nib_hi(yh), pb[g][n]);
-                            }
-                            xl >>= 8; xh >>= 8; yl >>= 8; yh >>= 8;
-                        }
+                        a[pc][0] = __byte_perm(w[0], w[1], 0x5410); a[pc][1] = __byte_perm(w[0], w[1], 0x7632);
+                        a[pc][2] = __byte_perm(w[2], w[3], 0x5410); a[pc][3] = __byte_perm(w[2], w[3], 0x7632);
                     } else {
                         const uint32_t sel = (r & 1) ? 0x7632 : 0x5410;
-                        uint32_t x = __byte_perm(w[0], w[1], sel), y = __byte_perm(w[2], w[3], sel);
+                        a[pc][0] = a[pc][1] = __byte_perm(w[0], w[1], sel);
+                        a[pc][2] = a[pc][3] = __byte_perm(w[2], w[3], sel);
+                    }
+                }
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {   // nibble 2j (rows r) and 2j + 1 (rows r + 8) of this lane's half word
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                weigh<EXACT, false, true>(acc[sb * 2 + j][n], nib_lo(x), nib_hi(x), nib_lo(y), nib_hi(y), pb[g][n]);
-                            x >>= 8; y >>= 8;
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (KS == 64) {   // nibbles 2j, 2j + 1 (rows r) and 2j + 4, 2j + 5 (rows r + 8)
+                            weigh<false, false>(acc[sb * 4 + 2 * j][n], a, pb[g][n], mid[n], flip);
+                            weigh<true, true>(acc[sb * 4 + 2 * j + 1][n], a, pb[g][n], mid[n], flip);
+                        } else {                    // nibble 2j (rows r) and 2j + 1 (rows r + 8) of this lane's half word
+                            weigh<false, true>(acc[sb * 2 + j][n], a, pb[g][n], mid[n], flip);
                         }
                     }
+#pragma unroll
+                    for (int pc = 0; pc < PCS; ++pc)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) a[pc][k] >>= 8;
                 }
             }
             __syncwarp();   // every lane has read the slot before it is refilled

@@ -456,6 +456,9 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
         // (scp); else they go through registers, which are stored with the next tile's issue.  (32 sequences of 500 to
         // 4096 tokens, 16 heads on 8 of 128, pages of 8: 47 us against 41 in pages of 64; each lookup and scale waited
         // for in its own tile took 108.  Pages of 1 and one group a head: 62 us.)
+        // Tokens before the first query's window share a tile with it, but not a page: theirs may be gone.
+        const int64_t w0 = (int64_t)sp.len - a.Tq - a.window + 1;
+        const int seen0 = a.window > 0 && w0 > 0 ? (int)w0 : 0;
         int64_t id_ahead[PCS];
         int sl_ahead[PCS], late_st = -1;
         uint16_t late[PCS][2][KG];
@@ -465,7 +468,7 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
                 const int t = tw + i * UNIT + pc * TILE + (lane & 15);
                 id_ahead[pc] = -1;
                 sl_ahead[pc] = 0;
-                if (i < nt && t < sp.len) {
+                if (i < nt && t < sp.len && t >= seen0) {
                     const int pg = t / a.S;
                     sl_ahead[pc] = t - pg * a.S;
                     id_ahead[pc] = __ldcg(pages + pg);
@@ -491,7 +494,8 @@ attention_kernel(const __grid_constant__ AttnArgs a) {
             for (int pc = 0; pc < PCS; ++pc) {
                 id[pc] = (uint64_t)id_ahead[pc] < (uint64_t)a.P ? (uint32_t)id_ahead[pc] : 0xffffffffu;
                 sl[pc] = sl_ahead[pc];
-                missing |= id[pc] == 0xffffffffu && tw + i * UNIT + pc * TILE + (lane & 15) < sp.len;
+                const int t = tw + i * UNIT + pc * TILE + (lane & 15);
+                missing |= id[pc] == 0xffffffffu && t < sp.len && t >= seen0;
             }
             fetch_rows(i + 1);
 #pragma unroll

@@ -333,7 +333,8 @@ aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots,
  *   first).  A sequence shorter than Tq leaves its first Tq - lengths[b] queries without a token
  *   to see; a query that sees nothing gives zeros.
  * pages: DEVICE pointer to int64 page ids, row b (at pages + b * pages_row) the pages of sequence
- *   b in order, max_pages of them; entries past a sequence's last page are not read.  A length
+ *   b in order, max_pages of them; entries past a sequence's last page, and of pages that lie before every
+ *   query's window, are not read.  A length
  *   outside [0, max_pages * S] is clamped, the tokens of a page id outside [0, P) count as
  *   zeros; both set the device error AQ_ERR_INDEX, and neither reads outside the cache.  Slots past a
  *   sequence's end may hold anything, NaN scales included.

@@ -31,3 +31,20 @@ def test_bounds_reject_results_that_leave_something_out(B, Hq, H, D, group, S, n
     swapped = pages.clone()
     swapped[:, -(n // S) // 2] = pages[:, 0]                                   # one page read twice, another not at all
     assert acc.misses(acc.attention(q, kc, vc, swapped, L, group)[0].to(dtype), want, bound, rms)[1] > acc.MARGIN
+
+
+def to_11_bits(x):
+    m, e = torch.frexp(x)
+    return torch.ldexp((m * 2.0 ** 11).round() / 2.0 ** 11, e)
+
+
+@pytest.mark.parametrize("D,group,S,n", [(128, 64, 64, 1500), (64, 32, 16, 700)])
+def test_bounds_reject_f16_results_from_one_f16_number_a_weight(D, group, S, n):
+    """p s carried in 11 bits, as bf16 outputs have it, is a miss for f16 ones."""
+    for dtype, fine in ((F16, False), (BF, True)):
+        pages, P = ref.page_table([n], S, 6)
+        kc, vc = ref.make_cache(P, 2, S, D, group, dtype, 1), ref.make_cache(P, 2, S, D, group, dtype, 2)
+        q = torch.randn(1, 1, 8, D, generator=torch.Generator().manual_seed(3)).to(dtype)
+        want, bound, rms = acc.attention(q, kc, vc, pages, [n], group)
+        got = acc.attention(q, kc, vc, pages, [n], group, weights=to_11_bits)[0]
+        assert (acc.misses(got.to(dtype), want, bound, rms)[1] < acc.MARGIN) == fine

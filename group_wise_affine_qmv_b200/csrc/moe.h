@@ -41,7 +41,8 @@ struct Args {
     float* xfac;                // [T]: what takes the sums back (and the RMS norm)
     // ... and by the gate/up kernel
     uint16_t* h;                // [T * topk, N] f16: weighted activations, a power of two per 16 columns, permuted;
-                                // where x is f16, what their rounding left over in T * topk rows more
+                                // in two parts, what their rounding left over in T * topk rows more
+    int parts;                  // of an activation: 1, or 2 where y is finer than bf16
     float* hscale;              // [T * topk, N / 16]: those powers of two
     unsigned* hmax;             // [T * topk]: the largest of each row's, as the bits of a float (zeroed by the first kernel)
     void* y;

@@ -29,7 +29,7 @@
 //    does an item alone, all of K, and ends with both sums of an activation in one lane.  Where there
 //    are too few items to fill the device the four warps of a CTA share one, a quarter of the stages each.
 //  - The activations pass on as f16 with a power of two per 16 of them (11 bits of mantissa where y has 8, two
-//    such numbers for f16: PARTS), and the largest of a row's powers (an atomic maximum: order does not matter), on which the
+//    such numbers where y is f16 or f32: parts_of), and the largest of a row's powers (an atomic maximum: order does not matter), on which the
 //    down kernel puts them, by one multiplication a pair, to multiply subnormal codes again.
 //  - x and the activations are read through L1: with few tokens all warps of the device walk the same lines, which
 //    from L2 cost up to 1.5 us a stage (one token: 53 against 42 us).
@@ -390,9 +390,9 @@ __device__ __forceinline__ void mma_step(float (&d0)[4], float (&d1)[4], float (
 
 // f16 numbers that an activation goes to the down product in: one for bf16 outputs, whose rounding is 8 times its
 // own; two (22 bits) for f16 outputs, whose rounding it would equal (2 tokens, 16 experts: 3.1e-4 off instead of
-// the 2.0e-4 of the output's rounding alone).
-template <typename XT>
-constexpr int PARTS = std::is_same<XT, f16_t>::value ? 2 : 1;
+// the 2.0e-4 of the output's rounding alone), and for f32 outputs, whatever x is (a bf16 x, 64 tokens, 4-bit experts: 2.1e-4
+// off in one part, 2.8e-5 in two, in 150 instead of 108 us).
+inline int parts_of(bool bf16, int ydt) { return bf16 && ydt == (int)DT::BF16 ? 1 : 2; }
 
 // The power of two 2^(e - 14) with 2^e above v, in f16's range around v.
 __device__ __forceinline__ float scale_for(float v) {
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
                     const uint16_t h0 = float_to_half_bits(u0, f16_t{}), h1 = float_to_half_bits(u1, f16_t{});
                     hp[code_pos<BITS>(r)] = h0;
                     hp[code_pos<BITS>(r + 8)] = h1;
-                    if constexpr (PARTS<XT> == 2) {
+                    if (std::is_same<XT, f16_t>::value || a.parts == 2) {
                         hp += (int64_t)a.T * a.topk * a.N;
                         hp[code_pos<BITS>(r)] = float_to_half_bits(u0 - half_bits_to_float(h0, f16_t{}), f16_t{});
                         hp[code_pos<BITS>(r + 8)] = float_to_half_bits(u1 - half_bits_to_float(h1, f16_t{}), f16_t{});
@@ -704,10 +704,11 @@ __global__ void __launch_bounds__(THREADS, 3) gate_up_kernel(const __grid_consta
 // ---- down ----
 
 // BLK: an entry's scales and biases come whole into one of two blocks that the CTA's warps share.
-template <int BITS, typename XT, int G, bool BLK>
+// P: parts of an activation.
+template <int BITS, typename XT, int G, bool BLK, int P>
 __global__ void __launch_bounds__(THREADS, 3) down_kernel(const __grid_constant__ Args a) {
     using Gm = Geo<BITS, G>;
-    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32, P = PARTS<XT>;
+    constexpr int GPS = Gm::GPS, XV = Gm::KS / 32;
     constexpr int NST = Gm::NST_DOWN, HALF = Gm::half(BLK), STAGE = 2 * HALF, SBB = Gm::SBB;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sb_full[2];
@@ -1054,6 +1055,7 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     // The down kernel's CTAs all at once on the device, one cluster of up to eight per 32 columns of y, no more
     // CTAs in it than there can be entries (64 tokens, 64 experts of 4 bits: 384 CTAs
     // of 444 that fit 116 us the layer, 512 CTAs 134).
+    a.parts = parts_of(std::is_same<XT, bf16_t>::value, a.ydt);
     const int blocks = (a.K + ROWS - 1) / ROWS;
     const int fit = 148 * (int)std::min<size_t>(3, 227 * 1024 / (smem_down + 1024));
     a.cs = std::max(1, std::min({8, fit / blocks, a.T * a.topk, a.E}));
@@ -1067,8 +1069,10 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
-            const void* fns[4] = {(const void*)gate_up_kernel<BITS, XT, G, false>, (const void*)gate_up_kernel<BITS, XT, G, true>,
-                                  (const void*)down_kernel<BITS, XT, G, false>, (const void*)down_kernel<BITS, XT, G, true>};
+            constexpr int P1 = std::is_same<XT, bf16_t>::value ? 1 : 2;
+            const void* fns[6] = {(const void*)gate_up_kernel<BITS, XT, G, false>, (const void*)gate_up_kernel<BITS, XT, G, true>,
+                                  (const void*)down_kernel<BITS, XT, G, false, P1>, (const void*)down_kernel<BITS, XT, G, true, P1>,
+                                  (const void*)down_kernel<BITS, XT, G, false, 2>, (const void*)down_kernel<BITS, XT, G, true, 2>};
             for (const void* f : fns) {
                 e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
                 if (e != cudaSuccess) return e;
@@ -1113,8 +1117,12 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)((a.K + ROWS - 1) / ROWS * a.cs));
     cfg.dynamicSmemBytes = smem_down;
     cfg.numAttrs = a.cs > 1 ? 2 : 1;
-    return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true>, a)
-                    : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false>, a);
+    if constexpr (std::is_same<XT, bf16_t>::value)
+        if (a.parts == 1)
+            return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true, 1>, a)
+                            : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false, 1>, a);
+    return blk_down ? cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, true, 2>, a)
+                    : cudaLaunchKernelEx(&cfg, down_kernel<BITS, XT, G, false, 2>, a);
 }
 
 template <int BITS, typename XT>

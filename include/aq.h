@@ -370,7 +370,7 @@ aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64
  * and makes its token's y NaN.
  * Every expert that some token chose is read once per 16 of its tokens; both contractions are exact
  * in W with fp32 sums; x enters exactly, and the weighted activations pass between the launches
- * with 11 bits of mantissa for AQ_BF16 x and 22 for AQ_F16 (relative to the largest of 16).  The
+ * with 11 bits of mantissa where y is AQ_BF16 and 22 where it is AQ_F16 or AQ_F32 (relative to the largest of 16).  The
  * same call gives the same bits; the order of a token's sum over its experts may depend on which
  * experts the other tokens chose.
  * workspace: DEVICE memory of at least the bytes aq_moe_swiglu_workspace(T, top_k, K, N) gives,

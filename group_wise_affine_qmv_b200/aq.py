@@ -363,6 +363,11 @@ def _ids(t: torch.Tensor, name: str, dim: int, device):
         raise TypeError(f"{name} must be contiguous")
 
 
+def _int32(v: int) -> int:
+    """The nearest 32-bit int: ctypes would take the low 32 bits, and 2**32 + 5 for 5."""
+    return max(-0x80000000, min(v, 0x7fffffff))
+
+
 def aq_kv_append(k, v, slots, k_cache, v_cache, group: int, bits: int, k_out=None, v_out=None):
     """New keys and values [T, H, D] into a paged cache: token t goes to slot slots[t] = page * S + offset
     (negative: not stored).  k_cache, v_cache = (wq [P, H, S, D*bits/32], scales, biases [P, H, S, D/group]),
@@ -397,7 +402,7 @@ def aq_kv_attention(q, k_cache, v_cache, pages, lengths, group: int, bits: int, 
         _check(lib, lib.aq_kv_attention_workspace(vq, vk, max_pages, ctypes.byref(need)))
         ws = q.new_empty(need.value, dtype=torch.uint8) if need.value else None
         _check(lib, lib.aq_kv_attention(vq, vk, *rest, group, bits, pages.data_ptr(), pages.stride(0), max_pages,
-                                        lengths.data_ptr(), scale, window, vo, ws.data_ptr() if need.value else None,
+                                        lengths.data_ptr(), scale, _int32(window), vo, ws.data_ptr() if need.value else None,
                                         need.value, stream))
     return out
 
@@ -410,6 +415,7 @@ def aq_moe_swiglu(x, logits, top_k: int, gate, up, down, group: int, bits: int, 
     lib = load_library()
     if out is None:
         out = torch.empty_like(x, dtype=out_dtype or x.dtype, memory_format=torch.contiguous_format)
+    top_k = _int32(top_k)
     with _On(x) as stream:
         need = ctypes.c_size_t()
         _check(lib, lib.aq_moe_swiglu_workspace(x.shape[0], top_k, x.shape[1], gate[0].shape[-2], ctypes.byref(need)))

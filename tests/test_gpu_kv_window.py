@@ -46,3 +46,18 @@ def test_a_page_that_a_query_sees_is_still_flagged():
     with pytest.raises(aq.AQError) as ei:
         aq.aq_device_error()
     assert ei.value.name == "AQ_ERR_INDEX"
+
+
+def test_a_window_past_32_bits_sees_every_token():
+    H, D, group, S, n, Tq = 2, 64, 32, 16, 77, 3
+    pages, P = ref.page_table([n], S, 1)
+    dev = [ref.to_dev(ref.make_cache(P, H, S, D, group, F16, s)) for s in (2, 3)]
+    q = torch.randn(1, Tq, 4, D, generator=torch.Generator().manual_seed(4)).to(F16).to(DEV)
+    run = lambda w: aq.aq_kv_attention(q, *dev, pages.to(DEV), torch.tensor([n], device=DEV), group, 4, window=w)
+    whole = run(0)
+    for w in (1 << 30, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, (1 << 63) - 1):
+        assert torch.equal(run(w), whole), w
+    for w in (-1, -(1 << 32) + 5):
+        with pytest.raises(aq.AQError):
+            run(w)
+    aq.aq_device_error()

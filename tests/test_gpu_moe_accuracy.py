@@ -65,3 +65,12 @@ def test_f32_outputs_do_not_depend_on_how_a_bf16_x_is_typed():
     want, _, rms = acc.layer(x, logits, top_k, [acc.Bank(s, group, bits) for s in sides], F32)
     for y in ys:
         assert (y - want).square().mean().sqrt() < acc.MARGIN * (rms.square().mean() + (2.0 ** -24 * want).square().mean()).sqrt()
+
+
+def test_top_k_past_32_bits_is_refused():
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    sides = [quantized(4, n, k, 64, 4, BF, gen) for n, k in ((64, 128), (64, 128), (128, 64))]
+    x = torch.randn(2, 128, generator=gen, device=DEV).to(BF)
+    for k in ((1 << 32) + 2, -(1 << 32) + 2):
+        with pytest.raises(aq.AQError):
+            aq.aq_moe_swiglu(x, torch.randn(2, 4, device=DEV), k, *sides, 64, 4)

@@ -26,7 +26,10 @@ AttnShape attn_shape(int64_t B, int64_t rows, int64_t Hkv, int D, int64_t max_to
     // CTAs that fit the device at once (the kernel's launch bounds)
     const int64_t all = (int64_t)SMS * ctas_per_sm(D, s.nt);
     const int64_t most = items * ((max_tokens + unit_tokens(D, s.nt) - 1) / unit_tokens(D, s.nt));
-    // Short contexts: an item per CTA, which spares the combine launch
+    // Short tables: an item per CTA, which spares the combine launch.  The rule goes by the table's width, which a
+    // captured step fixes, not by the lengths.  Tables of 512 (this form) and 528 tokens (the other), 16 heads on 8 of 128,
+    // bf16: one sequence of 128 tokens 5.4 and 6.7 us, of 512 9.2 and 7.3; 8 sequences of 300 8.3 and 9.4, of 512 9.7 and
+    // 9.6; 32 of 300 12.3 and 16.0, of 512 16.0 and 18.0; one of 512, D 256 15.7 and 8.3.  Wider tables cost what 528 does, within 1 us.
     if (max_tokens <= 512 && items <= 0x7fffffff) {
         s.split = 0;
         s.grid = (int)(items < 1 ? 1 : items);

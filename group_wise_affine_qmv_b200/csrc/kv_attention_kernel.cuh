@@ -18,7 +18,8 @@
 //    f16 subnormal n 2^-24 (low nibble) or n 2^-20 (high nibble), which the tensor cores take exactly.  So
 //    a pair of codes widens with one AND, and half the nibbles need no shift either.  The powers of two
 //    leave with q (keys: its odd dims are scaled by 1/16) and with the final outputs (values).  q itself is
-//    scaled by a power of two per row (its largest value near 2^14), so bf16 queries lose nothing as f16.
+//    scaled by a power of two per row (its largest value near 2^14): elements down to 2^-24 of that largest (bf16 2^-27) are
+//    exact as f16, smaller ones off by at most 2^-35 of it.
 //  - The order of dims inside an MMA is free as long as both operands agree; lanes read whole
 //    words, and q is stored permuted (0,4,1,5,2,6,3,7 within a word).
 //  - V^T needs pairs of tokens in one register: one PRMT per pair of words and half.
@@ -40,7 +41,7 @@
 //    Centred codes in one long accumulator do for channels around zero, but where some channels of a group lie far
 //    off, the others' codes are all small: f16, one channel of 32 at 20 deviations: the others 2.6e-3 off after 8192 tokens
 //    and 9.2e-2 after 131072; as it is 2.2e-4 and 4.6e-4 (rounding: 2.1e-4).  Without the mirror 3.0e-4 and 8.6e-4.  Cost: bf16
-//    3 to 5% (32 sequences of 9001 to 32768: 252 against 243 us), f16 0 to 4%.
+//    3 to 5% (32 sequences of 9001 to 32768: 250 against 243 us; 9% of a chunk of 512 queries over 4096 tokens), f16 0 to 4%.
 //  - f16 outputs carry p s as two f16 numbers (PARTS): one rounding of 11 bits for every term would equal the output's
 //    own.  131071 tokens, 32 heads on 8 of 128, group 128: 2.06e-4 off, the output's rounding 2.05e-4; bf16 in one part
 //    1.70e-3, its rounding 1.69e-3.
@@ -54,9 +55,11 @@
 // long sequences load the SMs alike.  A stretch that ends inside an item leaves a partial result
 // (at most two per CTA), which the combine kernel adds in CTA order; nothing depends on timing.
 //
-// Measured, device time of a call: 32 sequences of 500 to 4096 tokens, 16 heads on 8 of 128, bf16: 41.5 us, 2.0 TB/s; of 9001
-// to 32768, 32 heads on 8: 222 us, 3.4 TB/s (52% of a copy); one of 131071, f16: 56 us, 2.5 TB/s.  Bound by instructions: about
-// 660 a warp and tile of 32 tokens x 128, issue slots 44 to 52% busy at 11 warps an SM.
+// Measured, device time of a call: 32 sequences of 500 to 4096 tokens, 16 heads on 8 of 128, bf16: 43 us, 2.0 TB/s; of 9001
+// to 32768, 32 heads on 8: 250 us, 3.1 TB/s (47% of a copy); one of 131071, f16: 56 us, 2.5 TB/s.  Bound by latency at the 11 warps
+// an SM that registers allow: about 750 instructions a warp and tile of 32 tokens x 128, issue slots 46 to 56% busy, stalls on
+// fixed latencies and shared memory.  Instantiations for 16 and 32 query rows with groups of 32 spill, f16 most (D 128, 32
+// rows: 838 bytes of stores a thread; D 256, 16 rows: 750).
 #pragma once
 
 #include <cuda_bf16.h>

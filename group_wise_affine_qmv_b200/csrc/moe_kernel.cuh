@@ -13,8 +13,8 @@
 //    subnormals: a byte of a half, masked to one code, is already the f16 number code * 2^-24 (times 4 or
 //    16 where the code sits higher in the byte).  A pair of 8-bit codes takes one PRMT, a pair of 4-bit
 //    codes one AND and half a shift; the exact products and fp32 sums differ from those of the codes by
-//    powers of two only.  x is scaled by a power of two per token into f16's range (exact for bf16 and
-//    f16), its elements permuted and scaled to meet their codes' positions.
+//    powers of two only.  x is scaled by a power of two per token into f16's range (exact for elements
+//    down to 2^-24 of the token's largest, 2^-22 with 2-bit codes; smaller ones are off by at most 2^-33 of it), its elements permuted and scaled to meet their codes' positions.
 //  - A group costs s D + b X, two FMAs per row and token; X, the sum over the group, comes from one more MMA
 //    per k step whose codes are all one.  (Sums kept in memory by the kernel before and loaded per group took
 //    a third of the down kernel's time: 460 against 390 us for 32 tokens and 128 experts.)
@@ -38,10 +38,12 @@
 //    its first weights while the gate/up kernel still runs.  No atomics on results: nothing depends on
 //    timing.
 //
-// Measured, device time of a layer: one token, 8 of 128 experts of 8 bits, 1408 x 2816: 41 us, 2.6 TB/s (the first kernel
-// is 4 to 5 us of latency); 32 tokens, nearly the whole bank: 345 us, 4.3 TB/s; 64 tokens, 6 of 64 experts of 4 bits,
-// 2048 x 1024: 116 us, 1.9 TB/s.  The large kernels are bound by the latency of a stage (wait, shared memory, MMA, fold) at
-// the 12 warps an SM that their registers allow: 43% of the issue slots, 59% (gate/up) and 45% (down) of the DRAM peak.
+// Measured, device time of a layer: one token, 8 of 128 experts of 8 bits, 1408 x 2816: 40 us, 2.7 TB/s (the first kernel
+// is 4 to 5 us of latency); 32 tokens, nearly the whole bank: 354 us, 4.2 TB/s; 64 tokens, 6 of 64 experts of 4 bits,
+// 2048 x 1024: 116 us, 2.0 TB/s; the 128-expert bank in 2 bits, groups of 64: one token 47 us, 32 tokens 515 us, 0.8 TB/s.  The
+// large kernels are bound by the latency of a stage (wait, shared memory, MMA, fold) at the 10 to 12 warps an SM that
+// their registers allow: 37 to 43% of the issue slots, 20 to 59% of the DRAM peak.  Down kernels of activations in two parts spill
+// (4 bits 150 to 180 bytes of stores a thread, 2 bits 320 to 360), and of one part with 2 bits, groups of 64 (150).
 #pragma once
 
 #include <algorithm>
@@ -1095,7 +1097,9 @@ cudaError_t launch_t(Args a, cudaStream_t st) {
     cfg.blockDim = dim3(32 * PREP_WARPS);
     e = cudaLaunchKernelEx(&cfg, prep_kernel<BITS, XT>, a);
     if (e != cudaSuccess) return e;
-    // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM).  With no
+    // As many items as the tokens could choose, at most what fits the device at once (three CTAs an SM; two where a stage's scales
+    // take 8 bytes a row, 4 bits in groups of 32 or 2 bits in groups of 64, or a row has 54 groups or more: the last third of
+    // the grid then follows the first two).  With no
     // more items than CTAs that fit, four warps share an item: its latency counts, not the throughput (128 items, 16
     // experts of 4 bits: 13.6 against 16.4 us the layer; 512 items, 128 experts of 4 bits: 30.5 against 29.0; 1408 items,
     // of 8 bits: 48 against 41).  The same kernel takes rows whose scales do not fit a warp's block.

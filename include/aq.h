@@ -338,10 +338,13 @@ aq_status aq_kv_append(const aq_view* k, const aq_view* v, const int64_t* slots,
  *   outside [0, max_pages * S] is clamped, the tokens of a page id outside [0, P) count as
  *   zeros; both set the device error AQ_ERR_INDEX, and neither reads outside the cache.  Slots past a
  *   sequence's end may hold anything, NaN scales included.
+ *   Tables for up to 512 tokens (max_pages * S) take one launch, wider ones two, whatever the lengths: 32 sequences of 300
+ *   tokens run for 12 us with a table for 512 and 16 us with one for 4096.
  * workspace: DEVICE memory of at least the bytes aq_kv_attention_workspace gives for the same q,
  *   k_wq and max_pages, 16-byte aligned, used by this call only while it runs on its stream.
- * Scores, softmax statistics and sums are fp32; the query is exact, the product of a
- * probability and a value's scale is carried in 11 bits for AQ_BF16 and in 22 for AQ_F16.  Meant for decode and short runs of new
+ * Scores, softmax statistics and sums are fp32.  The elements of a query are exact down to 2^-24 of its largest and off by at
+ * most 2^-35 of that largest below; the product of a probability and a value's scale is carried in 11 bits for AQ_BF16 and in
+ * 22 for AQ_F16.  Meant for decode and short runs of new
  * tokens: the cache is read once per 32 query rows (D 256: 16) of a key/value head.
  */
 aq_status aq_kv_attention(const aq_view* q, const aq_view* k_wq, const aq_view* k_scales, const aq_view* k_biases,
@@ -369,7 +372,8 @@ aq_status aq_kv_attention_workspace(const aq_view* q, const aq_view* k_wq, int64
  * A token whose logits are all -inf gets y = r (0 without).  A NaN logit counts as the largest
  * and makes its token's y NaN.
  * Every expert that some token chose is read once per 16 of its tokens; both contractions are exact
- * in W with fp32 sums; x enters exactly, and the weighted activations pass between the launches
+ * in W with fp32 sums; x's elements are exact down to 2^-22 of their token's largest (off by at most 2^-33 of
+ * it below), and the weighted activations pass between the launches
  * with 11 bits of mantissa where y is AQ_BF16 and 22 where it is AQ_F16 or AQ_F32 (relative to the largest of 16).  The
  * same call gives the same bits; the order of a token's sum over its experts may depend on which
  * experts the other tokens chose.

@@ -60,6 +60,7 @@ def check(args, group, which=None, window=0, keep=slice(None)):
     (8, 64, 32, 65536, 0.0),
     (8, 256, 128, 32771, 0.0),
     (8, 128, 64, 8192, 20.0),
+    (8, 128, 64, 8192, -20.0),
     (8, 128, 32, 65536, 20.0),
 ])
 def test_a_long_context_in_one_cta(H, D, group, n, far, dtype):
